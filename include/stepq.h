@@ -448,6 +448,187 @@ STEPQ_API stepq_status stepq_calib_bits(int variant, int heads, double n_samples
                                         const int *widths, double avg_bits, double pivot_frac,
                                         uint8_t *bits);
 
+/* ---- serving: a batch's plan, its prompts, beam search ------------------- *
+ * What brings requests into a pool and moves them between its slots: the
+ * plan of a ragged batch (block table and slot map, built on the GPU from the
+ * request lengths), the prompt pass that turns many tokens of each request
+ * into a state and its readouts, the packing of those states into the slots
+ * of a pool, and beam search's selection with the reordering of the packed
+ * states.  The pages describe the decode step only; these entry points are
+ * what a runtime needs on either side of it.  The conventions at the top of
+ * this file hold, except that the tensors of a prompt and the logits may be
+ * fp32, binary16 or bfloat16. */
+
+/* Plain decayed linear attention, a third recurrence of the prompt entry
+ * point (pools hold Delta-rule states only): S = alpha S + k (beta v)^T. */
+#define STEPQ_LINEAR 2
+
+/* Element types of prompt tensors and logits. */
+#define STEPQ_F32 0
+#define STEPQ_F16 1
+#define STEPQ_BF16 2
+
+/* Tokens of a block of the plan. */
+#define STEPQ_BLOCK 64
+
+/* Largest requests, tokens and slots of a plan. */
+#define STEPQ_MAX_REQUESTS 65536
+#define STEPQ_MAX_TOKENS (1 << 28)
+#define STEPQ_MAX_SLOTS (1 << 24)
+
+/* Capacity of a plan. */
+typedef struct {
+    int requests; /* >= 0 */
+    int tokens;   /* rows of the batch's token tensors, >= 0 */
+    int slots;    /* state slots the requests' states live in, >= 0 */
+} stepq_plan_desc;
+
+/* Byte offsets of a plan's arrays from the start of its buffer, all int32.
+ * Entries past the built batch are -1 (starts: the end of the last request). */
+typedef struct {
+    size_t starts;         /* [requests + 1] first token row of each request */
+    size_t slot;           /* [requests] slot of each request (the slot map) */
+    size_t live;           /* [requests] the slot again, -1 where the request has no token or was refused */
+    size_t fresh;          /* [requests] 1: the state starts from zero (context 0) */
+    size_t token_request;  /* [tokens] request of each token row */
+    size_t token_position; /* [tokens] its place in the request's history */
+    size_t block_request;  /* [blocks] request of each block of STEPQ_BLOCK tokens (the block table) */
+    size_t block_first;    /* [blocks] the block's first token within its request */
+    size_t head;           /* [4] status bits, requests built, token rows used, blocks used */
+    size_t scratch;        /* the library's own */
+    size_t total;
+    int blocks;            /* tokens / STEPQ_BLOCK + requests */
+} stepq_plan_regions;
+STEPQ_API stepq_status stepq_plan_layout(const stepq_plan_desc *desc, stepq_plan_regions *out);
+
+/* Device bytes of a plan's buffer; 0 if the descriptor is invalid. */
+STEPQ_API size_t stepq_plan_bytes(const stepq_plan_desc *desc);
+
+/* Status bits of a plan (stepq_plan_check). */
+#define STEPQ_PLAN_BAD_LENGTH 1   /* a length below 0 (taken as 0) or above max_length (request refused) */
+#define STEPQ_PLAN_TOO_MANY 2     /* the lengths pass `tokens`: that request and all after it have no tokens */
+#define STEPQ_PLAN_BAD_SLOT 4     /* a slot out of range, or none for a request with a context (refused) */
+#define STEPQ_PLAN_SLOT_TWICE 8   /* two requests with tokens name one slot: the later ones are refused */
+#define STEPQ_PLAN_NO_SLOT 16     /* no free slot is left for a new request (refused) */
+
+/*
+ * Build the plan of a batch of n requests (n <= desc->requests) in the
+ * caller's buffer (16-byte aligned, stepq_plan_bytes), asynchronously.
+ * lengths: device int32 [n], the tokens of each request in this batch; the
+ * token tensors hold the requests' tokens one after the other.  contexts:
+ * device int32 [n], the tokens a request had before (0: a new request, whose
+ * state starts from zero), or NULL for none.  slots: device int32 [n], the
+ * slot of each request, or NULL for request r in slot r.  A slot of -1 asks
+ * for one: with busy (device uint8 [desc->slots], 0 = free, updated in place)
+ * the new requests (context 0) with tokens get the lowest free slots, in
+ * request order; slots the batch names count as used.  Without busy, -1 is
+ * refused.  max_length: an upper bound of the lengths (a longer request is
+ * refused).  A refused request has live = -1: later calls skip it and leave
+ * its rows and its state as they are.  One plan serves every layer of a
+ * model; it may be rebuilt in place, captured graphs included.  Two calls
+ * that build in one buffer, or share a busy map, must be ordered.
+ */
+STEPQ_API stepq_status stepq_plan_build(const stepq_plan_desc *desc, void *plan, size_t plan_bytes, int n,
+                                        const int *lengths, const int *contexts, const int *slots,
+                                        uint8_t *busy, int max_length, void *cuda_stream);
+
+/* Synchronise the stream and read the plan's status bits: STEPQ_OK when no
+ * request was refused, else STEPQ_ERR_INVALID_ARG with the reasons. */
+STEPQ_API stepq_status stepq_plan_check(const stepq_plan_desc *desc, const void *plan, size_t plan_bytes,
+                                        void *cuda_stream);
+
+/* A prompt pass over the batch of a plan. */
+typedef struct {
+    int variant;    /* STEPQ_GDN, STEPQ_KDA or STEPQ_LINEAR */
+    int dtype;      /* of q, k, v, out: STEPQ_F32, STEPQ_F16 or STEPQ_BF16 */
+    int heads;      /* value heads H (states per request), 1..65535 */
+    int heads_qk;   /* query and key heads, a divisor of H: value head h uses query and key head h / (H / heads_qk) */
+    int dk, dv;     /* 128 and 128 */
+    int max_length; /* the bound the plan was built with */
+    int by_slot;    /* 0: the state of request r is S[r]; 1: S[slot of r] */
+    long long stride_q, stride_k, stride_v; /* elements from one token row to the next; multiples of 16 bytes */
+} stepq_prompt_desc;
+
+/* Device scratch bytes of a prompt pass (0 is a valid answer when nothing is
+ * needed; (size_t)-1 if a descriptor is invalid). */
+STEPQ_API size_t stepq_prompt_scratch_bytes(const stepq_plan_desc *plan_desc, const stepq_prompt_desc *desc);
+
+/*
+ * The recurrence over all tokens of every live request of the plan:
+ *   S'_t = diag(alpha_t) S_(t-1)   (one alpha per head; per key row for KDA)
+ *   u_t  = beta_t (v_t - S'_t^T k_t)   (STEPQ_LINEAR: beta_t v_t)
+ *   S_t  = S'_t + k_t u_t^T,  out_t = S_t^T q_t
+ * -- stepq_fp32_step for a whole prompt.  q, k: device [tokens][heads_qk][dk]
+ * with the descriptor's token strides (rows of heads_qk * dk contiguous
+ * elements); v: [tokens][heads][dv] likewise; alpha: device fp32
+ * [tokens][heads], or [tokens][heads][dk] for KDA; beta: device fp32
+ * [tokens][heads]; out: device [tokens][heads][dv], contiguous.  S: device
+ * fp32 [requests or slots][heads][dk][dv], updated in place; a fresh request
+ * starts from zero and its old content is not read.  Rows past the last
+ * request's tokens, and the rows and states of requests without tokens or
+ * refused, are neither read nor written.  alpha in [0, 1].  Arithmetic and
+ * the state are fp32 (products on tensor cores are split so that their
+ * rounding stays at that level); out is rounded once.  scratch: device,
+ * 256-byte aligned, at least stepq_prompt_scratch_bytes, not shared by two
+ * calls in flight.  out must not alias an input.  The plan must have been
+ * built with at most desc->max_length tokens a request; with a bound of
+ * STEPQ_STEP_TOKENS or less the pass runs the recurrence token by token (the
+ * form for single tokens), otherwise in blocks of STEPQ_BLOCK tokens.
+ */
+#define STEPQ_STEP_TOKENS 8
+STEPQ_API stepq_status stepq_prompt(const stepq_plan_desc *plan_desc, const void *plan, size_t plan_bytes,
+                                    const stepq_prompt_desc *desc, const void *q, const void *k, const void *v,
+                                    const float *alpha, const float *beta, float *S, void *out, void *scratch,
+                                    size_t scratch_bytes, void *cuda_stream);
+
+/*
+ * stepq_pack for the live requests of a plan: the state of request r goes to
+ * the pool's request slot live[r]; the pool's other requests are neither read
+ * nor written.  S: device fp32, state r at S[r] (by_slot 0) or S[live[r]]
+ * (by_slot 1).  plan_desc->slots must equal the pool's batch.
+ */
+STEPQ_API stepq_status stepq_pack_requests(stepq_pool *pool, const stepq_plan_desc *plan_desc, const void *plan,
+                                           size_t plan_bytes, const float *S, int by_slot);
+
+/* Largest beams of a group and candidates of a selection. */
+#define STEPQ_MAX_BEAMS 64
+
+/* Device scratch bytes of stepq_beam_select (0 if the sizes are invalid). */
+STEPQ_API size_t stepq_beam_scratch_bytes(int groups, int beams, int vocab, int n);
+
+/*
+ * Beam search's selection: in each group the n best continuations (1 <= n <=
+ * STEPQ_MAX_BEAMS) of its beams, by score = scores[g][b] + log_softmax(
+ * logits[g][b])[token], best first.  Scores are compared in 64 bits and
+ * rounded to fp32 on return; equal scores go to the lowest beam, then the
+ * lowest token.  A candidate whose logit is -inf or NaN, or whose beam's score
+ * is -inf or NaN, is none; where fewer than n are left the rest of the outputs
+ * is score -inf, parent -1, token -1.  A logit of +inf takes all of its row's
+ * probability (shared by equals).  logits: device [groups][beams] rows of
+ * vocab contiguous elements of the given type, `stride` elements apart
+ * (>= vocab); scores: device fp32 [groups][beams].  Outputs, device
+ * [groups][n]: scores_out fp32, parents and tokens int32; they must not alias
+ * the inputs.  scratch: device, 16-byte aligned, not shared by two calls in
+ * flight.
+ */
+STEPQ_API stepq_status stepq_beam_select(int groups, int beams, int vocab, int n, int dtype, const void *logits,
+                                         long long stride, const float *scores, float *scores_out, int *parents,
+                                         int *tokens, void *scratch, size_t scratch_bytes, void *cuda_stream);
+
+/*
+ * Reorder rows inside groups, in place: row g * beams + i becomes what row
+ * g * beams + parents[g][i] was; a parent outside 0 .. beams-1
+ * leaves its row.  base: device, 16-byte aligned; row_bytes a multiple of 16;
+ * parents: device int32 [groups][beams].  Only rows that change are read and
+ * written.
+ */
+STEPQ_API stepq_status stepq_reorder_rows(void *base, size_t row_bytes, int groups, int beams, const int *parents,
+                                          void *cuda_stream);
+
+/* The same for a pool's packed states, on the pool's stream: rows are
+ * requests, groups of `beams` requests from request `first` on. */
+STEPQ_API stepq_status stepq_pool_reorder(stepq_pool *pool, int first, int groups, int beams, const int *parents);
+
 /* Human-readable name of a status; never NULL. */
 STEPQ_API const char *stepq_status_string(stepq_status s);
 

@@ -13,35 +13,10 @@
 #include <string>
 #include <vector>
 
-#include "stepq.h"
-#include "stepq_internal.cuh"
+#include "stepq_host.cuh"
 
 using stepq::kDK;
 using stepq::kDV;
-
-struct stepq_pool {
-    stepq_desc desc;  // table pointers cleared; the tables are copied below
-    std::vector<uint8_t> bits;
-    std::vector<float> rho;
-    uint8_t *dev = nullptr;
-    size_t bytes = 0, state_bytes = 0;
-    long long req_bytes = 0;
-    cudaStream_t stream = nullptr;
-    stepq::Tables t{};
-    int n_pivot_items = 0;
-    int max_n16 = 0;  // the most leading 16-bit field positions of a staged head
-    int scale_mode = STEPQ_SCALE_DUAL;
-    int nslots = 0, slot_bytes = 0;
-    int off_q = 0, off_k = 0, off_v = 0, off_alpha = 0, off_ab = 0, off_rec = 0;
-    // the active request set: decode steps update requests active[0..n_active)
-    int n_active = 0;
-    std::vector<int> kind;               // per head: kHeadQuant / kHeadAllPivot / kHeadMixed
-    std::vector<long long> item_bytes;   // per head
-    std::vector<long long> head_off;     // per head
-    std::vector<int> active_tables;      // host copy of the uploaded order and staging records
-    size_t guard[7] = {};                // offsets of the guard regions (kGuardRegions)
-    size_t total = 0;                    // bytes of the pool's regions, guards included
-};
 
 namespace {
 
@@ -49,7 +24,11 @@ thread_local std::string g_err;
 std::mutex g_live_mu;
 std::set<const stepq_pool *> g_live;
 
-stepq_status fail(stepq_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+}  // namespace
+
+namespace stepq {
+namespace host {
+
 stepq_status fail(stepq_status s, const char *fmt, ...)
 {
     char buf[512];
@@ -60,6 +39,13 @@ stepq_status fail(stepq_status s, const char *fmt, ...)
     g_err = buf;
     return s;
 }
+
+}  // namespace host
+}  // namespace stepq
+
+using namespace stepq::host;
+
+namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -241,6 +227,11 @@ stepq_status check_desc(const stepq_desc *d, bool need_tables, Layout *L)
     return STEPQ_OK;
 }
 
+}  // namespace
+
+namespace stepq {
+namespace host {
+
 stepq_status check_pool(const stepq_pool *p)
 {
     if (!p) return fail(STEPQ_ERR_INVALID_ARG, "pool is NULL");
@@ -298,6 +289,11 @@ stepq::StepArgs base_args(const stepq_pool *p)
     a.state_bytes = (long long)p->state_bytes;
     return a;
 }
+
+}  // namespace host
+}  // namespace stepq
+
+namespace {
 
 // Item order and staging records of a decode step over the requests
 // active[0 .. n_active) (all requests in order when active is NULL): position

@@ -89,6 +89,10 @@ struct StepArgs {
     const float *q, *k, *v, *alpha, *beta;
     float *out;
     const float *S_in;  // pack
+    // pack by request: item r * heads + h goes to slot live[r] (< 0: none),
+    // from S_in's state r, or from state live[r] with by_slot; null = all slots
+    const int *live;
+    int by_slot;
     float *S_out;       // unpack
 };
 

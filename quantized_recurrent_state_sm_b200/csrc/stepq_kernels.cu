@@ -1332,8 +1332,14 @@ __global__ void __launch_bounds__(kThreads) k_pack(StepArgs a)
     __shared__ ItemSmem sm;
     STEPQ_RETURN_IF_REJECTED(a);
     RowFactors &rf = sm.u.rf[0];
-    const int item = blockIdx.x;
-    const int rq = item / a.heads, h = item - rq * a.heads;
+    int item = blockIdx.x;
+    int rq = item / a.heads;
+    const int h = item - rq * a.heads;
+    if (a.live) {
+        rq = a.live[rq];
+        if (rq < 0 || rq >= a.batch) return;
+        if (a.by_slot) item = rq * a.heads + h;
+    }
     const HeadRec *rec = a.t.rowrec + h;
     load_head(rf, rec);
     __syncthreads();

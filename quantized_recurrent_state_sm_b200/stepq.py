@@ -20,10 +20,14 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 CHECK_BUILD = os.environ.get("STEPQ_CHECK", "0") == "1"
 LIB_PATH = os.path.join(_HERE, "libstepq_check.so" if CHECK_BUILD else "libstepq.so")
 
-GDN, KDA = 0, 1
+GDN, KDA, LINEAR = 0, 1, 2
 SCALE_DUAL, SCALE_ROW, SCALE_COL, SCALE_HEAD = 0, 1, 2, 3
 PIVOT_BITS = 16
 DK = DV = 128
+BLOCK = 64        # tokens of a block of a plan
+STEP_TOKENS = 8   # prompts of at most this many tokens run token by token
+MAX_BEAMS = 64
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_STATE = 0, 1, 2, 3, 4
 
@@ -53,12 +57,29 @@ class CalibDesc(C.Structure):
                 ("pivot_frac", C.c_double)]
 
 
+class PlanDesc(C.Structure):
+    _fields_ = [("requests", C.c_int), ("tokens", C.c_int), ("slots", C.c_int)]
+
+
+class PlanRegions(C.Structure):
+    _fields_ = [(f, C.c_size_t) for f in ("starts", "slot", "live", "fresh", "token_request", "token_position",
+                                          "block_request", "block_first", "head", "scratch", "total")] + [("blocks", C.c_int)]
+
+
+class PromptDesc(C.Structure):
+    _fields_ = [(f, C.c_int) for f in ("variant", "dtype", "heads", "heads_qk", "dk", "dv", "max_length", "by_slot")] + [
+        (f, C.c_longlong) for f in ("stride_q", "stride_k", "stride_v")]
+
+
 EXPORTS = ("stepq_pool_bytes", "stepq_state_bytes", "stepq_pool_layout", "stepq_pool_check_guards", "stepq_pool_create", "stepq_pool_destroy",
            "stepq_pool_set_stream", "stepq_pack", "stepq_unpack", "stepq_decode_step",
            "stepq_fp32_step", "stepq_pool_check", "stepq_status_string", "stepq_last_error", "stepq_selftest_bounded_wait",
            "stepq_decode_step_noalloc", "stepq_decode_step_split", "stepq_pool_set_active",
            "stepq_pool_set_scale_mode", "stepq_calib_scratch_bytes", "stepq_calibrate", "stepq_calib_accumulate", "stepq_calib_row_error",
-           "stepq_calib_reduce", "stepq_calib_rho", "stepq_calib_bits")
+           "stepq_calib_reduce", "stepq_calib_rho", "stepq_calib_bits",
+           "stepq_plan_layout", "stepq_plan_bytes", "stepq_plan_build", "stepq_plan_check", "stepq_prompt_scratch_bytes",
+           "stepq_prompt", "stepq_pack_requests", "stepq_beam_scratch_bytes", "stepq_beam_select", "stepq_reorder_rows",
+           "stepq_pool_reorder")
 
 
 def _load():
@@ -92,6 +113,21 @@ def _load():
     L.stepq_calib_reduce.argtypes = [i, i, i, P, P, P]
     L.stepq_calib_rho.argtypes = [i, dbl, P, P]
     L.stepq_calib_bits.argtypes = [i, i, dbl, P, P, P, i, P, dbl, dbl, P]
+    PD, z, ll = C.POINTER(PlanDesc), C.c_size_t, C.c_longlong
+    L.stepq_plan_layout.argtypes = [PD, C.POINTER(PlanRegions)]
+    L.stepq_plan_bytes.argtypes = [PD]; L.stepq_plan_bytes.restype = z
+    L.stepq_plan_build.argtypes = [PD, P, z, i, P, P, P, P, i, P]
+    L.stepq_plan_check.argtypes = [PD, P, z, P]
+    L.stepq_prompt_scratch_bytes.argtypes = [PD, C.POINTER(PromptDesc)]; L.stepq_prompt_scratch_bytes.restype = z
+    L.stepq_prompt.argtypes = [PD, P, z, C.POINTER(PromptDesc), P, P, P, P, P, P, P, P, z, P]
+    L.stepq_pack_requests.argtypes = [P, PD, P, z, P, i]
+    L.stepq_beam_scratch_bytes.argtypes = [i, i, i, i]; L.stepq_beam_scratch_bytes.restype = z
+    L.stepq_beam_select.argtypes = [i, i, i, i, i, P, ll, P, P, P, P, P, z, P]
+    L.stepq_reorder_rows.argtypes = [P, z, i, i, P, P]
+    L.stepq_pool_reorder.argtypes = [P, i, i, i, P]
+    for fn in ("stepq_plan_layout", "stepq_plan_build", "stepq_plan_check", "stepq_prompt", "stepq_pack_requests",
+               "stepq_beam_select", "stepq_reorder_rows", "stepq_pool_reorder"):
+        getattr(L, fn).restype = C.c_int
     for fn in ("stepq_pool_create", "stepq_pool_destroy", "stepq_pool_set_stream", "stepq_pool_check",
                "stepq_selftest_bounded_wait", "stepq_pack",
                "stepq_unpack", "stepq_decode_step", "stepq_fp32_step", "stepq_decode_step_noalloc",
@@ -245,6 +281,41 @@ class PackedStatePool:
                                            _dev(beta, "beta", (B, H)), _dev(out, "out", (B, H, DV)), side))
         return out
 
+    def pack_requests(self, plan: "RequestPlan", S: torch.Tensor, by_slot: bool = False):
+        """Pack the states of the plan's live requests into their slots; the
+        pool's other requests stay as they are.  S: [requests, heads, 128, 128]
+        (state r of request r), or with by_slot [batch, heads, 128, 128]."""
+        rows = self.batch if by_slot else plan.requests
+        self._sync_stream()
+        _check(lib.stepq_pack_requests(self._h, C.byref(plan._desc), C.c_void_p(plan.buffer.data_ptr()), plan.nbytes,
+                                       _dev(S, "S", (rows, self.heads, DK, DV)), int(by_slot)))
+
+    def reorder(self, parents: torch.Tensor, first: int = 0):
+        """Reorder packed states inside groups, in place: with parents [groups,
+        beams] (int32 CUDA), request first + g * beams + i becomes what request
+        first + g * beams + parents[g, i] was (a parent outside the group's
+        beams, as -1, leaves it)."""
+        if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+            raise ValueError("parents must have shape [groups, beams]")
+        G, B = parents.shape
+        self._sync_stream()
+        _check(lib.stepq_pool_reorder(self._h, int(first), G, B, _dev_any(parents, "parents", torch.int32, (G, B))))
+
+    def beam_step(self, logits: torch.Tensor, scores: torch.Tensor, first: int = 0):
+        """One step of a beam search over the pool: select the best `beams`
+        continuations of each group (beam_select) and give each new beam the
+        state of its parent (reorder).  logits [groups, beams, vocab], scores
+        [groups, beams]; request first + g * beams + i holds the state of beam
+        i of group g.  Returns (scores, parents, tokens), each [groups, beams]."""
+        if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+            raise ValueError("logits must have shape [groups, beams, vocab]")
+        G, B = logits.shape[:2]
+        if first < 0 or first + G * B > self.batch:
+            raise ValueError(f"{G} groups of {B} beams from request {first} pass the pool's {self.batch} requests")
+        got = beam_select(logits, scores)
+        self.reorder(got[1], first)
+        return got
+
     def check(self):
         """Synchronise the pool's stream and raise if a kernel reported an error."""
         self._sync_stream()
@@ -326,8 +397,6 @@ def selftest_bounded_wait(limit_cycles: int, arrive: bool, device=None) -> tuple
     return r[0], r[1]
 
 
-# ---- calibration -------------------------------------------------------------
-
 def _dev_any(t: torch.Tensor, name: str, dtype, shape) -> C.c_void_p:
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a {dtype} CUDA tensor")
@@ -337,6 +406,162 @@ def _dev_any(t: torch.Tensor, name: str, dtype, shape) -> C.c_void_p:
         raise ValueError(f"{name} must be contiguous")
     return C.c_void_p(t.data_ptr())
 
+
+# ---- serving: plans, prompts, beam search --------------------------------------
+
+class RequestPlan:
+    """The plan of a ragged batch: block table and slot map, built on the GPU.
+
+    Holds room for `requests` requests with `tokens` token rows in all, whose
+    states live in `slots` slots (default: one each).  After build() the int32
+    views starts [requests + 1], slots and live [requests], fresh [requests],
+    token_request and token_position [tokens], block_request and block_first
+    [blocks] describe the batch (include/stepq.h, stepq_plan_regions).
+    """
+
+    def __init__(self, requests: int, tokens: int, slots: int | None = None, device=None):
+        self.requests, self.tokens = int(requests), int(tokens)
+        self.n_slots = self.requests if slots is None else int(slots)
+        self.max_length = self.tokens
+        self._desc = PlanDesc(self.requests, self.tokens, self.n_slots)
+        r = PlanRegions()
+        _check(lib.stepq_plan_layout(C.byref(self._desc), C.byref(r)))
+        self.nbytes, self.blocks = int(r.total), int(r.blocks)
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        self.buffer = torch.empty(max(self.nbytes, 16), dtype=torch.uint8, device=dev)
+        ints = self.buffer[:self.nbytes].view(torch.int32)
+
+        def view(offset, n):
+            return ints[offset // 4: offset // 4 + n]
+
+        self.head = view(r.head, 4)
+        self.starts = view(r.starts, self.requests + 1)
+        self.slots, self.live, self.fresh = (view(o, self.requests) for o in (r.slot, r.live, r.fresh))
+        self.token_request, self.token_position = (view(o, self.tokens) for o in (r.token_request, r.token_position))
+        self.block_request, self.block_first = (view(o, self.blocks) for o in (r.block_request, r.block_first))
+
+    def build(self, lengths: torch.Tensor, contexts: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+              busy: torch.Tensor | None = None, max_length: int | None = None) -> "RequestPlan":
+        """Build the plan of a batch (stepq_plan_build), asynchronously on the
+        current stream.  lengths, contexts, slots: int32 CUDA tensors of one
+        entry a request; busy: uint8 CUDA map of the used slots, from which
+        slots of -1 are served and which is updated; max_length: an upper bound
+        of the lengths (default: the plan's tokens)."""
+        n = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else -1
+        ptr = [_dev_any(lengths, "lengths", torch.int32, (max(n, 0),))]
+        for t, name in ((contexts, "contexts"), (slots, "slots")):
+            ptr.append(None if t is None else _dev_any(t, name, torch.int32, (n,)))
+        ptr.append(None if busy is None else _dev_any(busy, "busy", torch.uint8, (self.n_slots,)))
+        bound = self.tokens if max_length is None else int(max_length)
+        _check(lib.stepq_plan_build(C.byref(self._desc), C.c_void_p(self.buffer.data_ptr()), self.nbytes, n, *ptr, bound,
+                                    _stream_ptr()))
+        self.max_length = bound
+        return self
+
+    def check(self):
+        """Synchronise the current stream and raise if the plan refused a request."""
+        _check(lib.stepq_plan_check(C.byref(self._desc), C.c_void_p(self.buffer.data_ptr()), self.nbytes, _stream_ptr()))
+
+
+def _rows(t: torch.Tensor, name: str, dtype, tokens: int, heads: int):
+    """A [tokens, heads, 128] tensor whose rows of heads * 128 are contiguous: (pointer, token stride)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if t.dim() != 3 or tuple(t.shape) != (tokens, heads, DK):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(tokens, heads, DK)}")
+    if tokens > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != DK)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return C.c_void_p(t.data_ptr()), (t.stride(0) if tokens > 1 else heads * DK)
+
+
+def prompt(variant: int, plan: RequestPlan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: torch.Tensor,
+           beta: torch.Tensor, S: torch.Tensor, out: torch.Tensor | None = None, by_slot: bool = False) -> torch.Tensor:
+    """The recurrence over all tokens of the plan's requests (stepq_prompt).
+
+    variant GDN, KDA (the gated Delta rule) or LINEAR (decayed linear
+    attention); q, k [tokens, heads_qk, 128] and v [tokens, heads, 128] in
+    float32, float16 or bfloat16, token rows possibly strided, heads a multiple
+    of heads_qk; alpha [tokens, heads] or [tokens, heads, 128] (KDA) and beta
+    [tokens, heads] float32; S float32 [requests, heads, 128, 128], or with
+    by_slot [slots, heads, 128, 128], updated in place.  Returns out [tokens,
+    heads, 128] in the type of q; rows of no request keep what `out` held."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in _DTYPES:
+        raise TypeError("q must be a float32, float16 or bfloat16 CUDA tensor")
+    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("q and v must have shape [tokens, heads, 128]")
+    T, Hk, H, dt = plan.tokens, q.shape[1], v.shape[1], q.dtype
+    (qp, qs), (kp, ks) = _rows(q, "q", dt, T, Hk), _rows(k, "k", dt, T, Hk)
+    vp, vs = _rows(v, "v", dt, T, H)
+    d = PromptDesc(variant, _DTYPES[dt], H, Hk, DK, DV, plan.max_length, int(by_slot), qs, ks, vs)
+    ap = _dev(alpha, "alpha", (T, H, DK) if variant == KDA else (T, H))
+    bp = _dev(beta, "beta", (T, H))
+    Sp = _dev(S, "S", (plan.n_slots if by_slot else plan.requests, H, DK, DV))
+    if out is None:
+        out = torch.empty((T, H, DV), dtype=dt, device=q.device)
+    op = _dev_any(out, "out", dt, (T, H, DV))
+    need = lib.stepq_prompt_scratch_bytes(C.byref(plan._desc), C.byref(d))
+    if need == C.c_size_t(-1).value:
+        _check(ERR_INVALID_ARG)
+    # from torch's allocator, so that calls on several streams or in several graphs have their own
+    scratch = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _check(lib.stepq_prompt(C.byref(plan._desc), C.c_void_p(plan.buffer.data_ptr()), plan.nbytes, C.byref(d), qp, kp, vp, ap,
+                            bp, Sp, op, C.c_void_p(scratch.data_ptr()) if need else None, need, _stream_ptr()))
+    return out
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None):
+    """The n (default: beams) best continuations of each group's beams
+    (stepq_beam_select): logits [groups, beams, vocab] in float32, float16 or
+    bfloat16, rows possibly strided; scores float32 [groups, beams].  Returns
+    (scores float32, parents int32, tokens int32), each [groups, n], best
+    first; score -inf, parent -1 and token -1 where no candidate is left."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _DTYPES or not logits.is_cuda:
+        raise TypeError("logits must be a float32, float16 or bfloat16 CUDA tensor")
+    if logits.dim() != 3:
+        raise ValueError("logits must have shape [groups, beams, vocab]")
+    G, B, V = logits.shape
+    n = B if n is None else int(n)
+    sp = _dev(scores, "scores", (G, B))
+    if V > 0 and logits.stride(2) != 1:
+        raise ValueError("logits: a row's tokens must be contiguous")
+    stride = logits.stride(1) if B > 1 else (logits.stride(0) if G > 1 else V)
+    if G > 1 and B > 1 and logits.stride(0) != B * stride:
+        raise ValueError("logits: rows must be evenly spaced")
+    dev = logits.device
+    out = (torch.empty((G, n), dtype=torch.float32, device=dev), torch.empty((G, n), dtype=torch.int32, device=dev),
+           torch.empty((G, n), dtype=torch.int32, device=dev)) if n >= 0 else ()
+    if not out:
+        raise ValueError("n must be positive")
+    need = lib.stepq_beam_scratch_bytes(G, B, V, n)
+    if need == 0:
+        _check(ERR_INVALID_ARG)
+    scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+    _check(lib.stepq_beam_select(G, B, V, n, _DTYPES[logits.dtype], C.c_void_p(logits.data_ptr()), stride, sp,
+                                 *(C.c_void_p(t.data_ptr()) for t in out), C.c_void_p(scratch.data_ptr()), need, _stream_ptr()))
+    return out
+
+
+def reorder_rows(rows: torch.Tensor, parents: torch.Tensor):
+    """Reorder rows inside groups, in place (stepq_reorder_rows): with parents
+    [groups, beams] (int32 CUDA), row g * beams + i of the contiguous CUDA
+    tensor rows [groups * beams, ...] becomes what row g * beams + parents[g, i]
+    was -- unquantised states, convolution windows, token histories."""
+    if not isinstance(rows, torch.Tensor) or not rows.is_cuda or rows.dim() < 1:
+        raise TypeError("rows must be a CUDA tensor")
+    if not isinstance(parents, torch.Tensor) or parents.dim() != 2:
+        raise ValueError("parents must have shape [groups, beams]")
+    G, B = parents.shape
+    if rows.shape[0] != G * B:
+        raise ValueError(f"rows has {rows.shape[0]} rows, expected {G * B}")
+    if not rows.is_contiguous():
+        raise ValueError("rows must be contiguous")
+    nbytes = rows.numel() // max(G * B, 1) * rows.element_size()
+    _check(lib.stepq_reorder_rows(C.c_void_p(rows.data_ptr()), nbytes, G, B,
+                                  _dev_any(parents, "parents", torch.int32, (G, B)), _stream_ptr()))
+    return rows
+
+
+# ---- calibration -------------------------------------------------------------
 
 def _host(a, dtype):
     a = np.ascontiguousarray(a, dtype=dtype)
