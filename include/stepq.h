@@ -484,7 +484,7 @@ typedef struct {
 } stepq_plan_desc;
 
 /* Byte offsets of a plan's arrays from the start of its buffer, all int32.
- * Entries past the built batch are -1 (starts: the end of the last request). */
+ * Entries past the built batch are -1 (starts, block_starts: the end of the last request). */
 typedef struct {
     size_t starts;         /* [requests + 1] first token row of each request */
     size_t slot;           /* [requests] slot of each request (the slot map) */
@@ -492,6 +492,7 @@ typedef struct {
     size_t fresh;          /* [requests] 1: the state starts from zero (context 0) */
     size_t token_request;  /* [tokens] request of each token row */
     size_t token_position; /* [tokens] its place in the request's history */
+    size_t block_starts;   /* [requests + 1] first block of each request */
     size_t block_request;  /* [blocks] request of each block of STEPQ_BLOCK tokens (the block table) */
     size_t block_first;    /* [blocks] the block's first token within its request */
     size_t head;           /* [4] status bits, requests built, token rows used, blocks used */
@@ -510,6 +511,7 @@ STEPQ_API size_t stepq_plan_bytes(const stepq_plan_desc *desc);
 #define STEPQ_PLAN_BAD_SLOT 4     /* a slot out of range, or none for a request with a context (refused) */
 #define STEPQ_PLAN_SLOT_TWICE 8   /* two requests with tokens name one slot: the later ones are refused */
 #define STEPQ_PLAN_NO_SLOT 16     /* no free slot is left for a new request (refused) */
+#define STEPQ_PLAN_TIMEOUT 32     /* a prompt kernel's bounded wait for a copy gave up (about two seconds) */
 
 /*
  * Build the plan of a batch of n requests (n <= desc->requests) in the
@@ -533,7 +535,8 @@ STEPQ_API stepq_status stepq_plan_build(const stepq_plan_desc *desc, void *plan,
                                         uint8_t *busy, int max_length, void *cuda_stream);
 
 /* Synchronise the stream and read the plan's status bits: STEPQ_OK when no
- * request was refused, else STEPQ_ERR_INVALID_ARG with the reasons. */
+ * request was refused, else STEPQ_ERR_INVALID_ARG with the reasons
+ * (STEPQ_ERR_CUDA after a wait that gave up in a prompt over this plan). */
 STEPQ_API stepq_status stepq_plan_check(const stepq_plan_desc *desc, const void *plan, size_t plan_bytes,
                                         void *cuda_stream);
 

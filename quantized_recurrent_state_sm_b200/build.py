@@ -14,8 +14,9 @@ LIB = os.path.join(HERE, "libstepq.so")
 # the checking build (kernels validate the pool's tables before touching
 # memory; see stepq_pool_check_guards in include/stepq.h)
 LIB_CHECK = os.path.join(HERE, "libstepq_check.so")
-SOURCES = ["stepq_abi.cu", "stepq_kernels.cu", "stepq_serve_abi.cu", "stepq_plan.cu", "stepq_prompt.cu", "stepq_beam.cu"]
-HEADERS = ["stepq_internal.cuh", "stepq_device.cuh", "stepq_host.cuh", "stepq_serve.cuh"]
+SOURCES = ["stepq_abi.cu", "stepq_kernels.cu", "stepq_serve_abi.cu", "stepq_plan.cu", "stepq_prompt.cu",
+           "stepq_prompt_blocks.cu", "stepq_beam.cu"]
+HEADERS = ["stepq_internal.cuh", "stepq_device.cuh", "stepq_host.cuh", "stepq_serve.cuh", "stepq_mma.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

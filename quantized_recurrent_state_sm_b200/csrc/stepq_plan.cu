@@ -100,12 +100,13 @@ __device__ void resolve(const PlanArgs &a, int r0, int r1, Pair at, Pair *sm, in
         const Pair end = add(at, {len, blocks_of(len)});
         const bool fits = end.tokens <= (unsigned)p.tokens;
         if (fits) {
-            if (r == 0) p.starts[0] = 0;
+            if (r == 0) p.starts[0] = p.block_starts[0] = 0;
             p.starts[r + 1] = (int)end.tokens;
+            p.block_starts[r + 1] = (int)end.blocks;
             rows = end.tokens;
             blocks = end.blocks;
         } else {
-            if (r == 0) p.starts[0] = 0;
+            if (r == 0) p.starts[0] = p.block_starts[0] = 0;
             p.starts[r + 1] = -1;  // set to the last end below
             bad |= kPlanTooMany;
         }
@@ -136,14 +137,17 @@ __device__ void resolve(const PlanArgs &a, int r0, int r1, Pair at, Pair *sm, in
         p.fresh[r] = 0;
         p.starts[r + 1] = -1;
     }
-    if (a.n == 0 && tid == 0) p.starts[0] = 0;
+    if (a.n == 0 && tid == 0) p.starts[0] = p.block_starts[0] = 0;
     if (rows) atomicMax(&rows_used, rows);
     if (blocks) atomicMax(&blocks_used, blocks);
     if (bad) atomicOr(flags, bad);
     Pair all;
     Pair rank = block_scan({need, 0}, sm, &all);  // orders the writes above, too
     for (int r = tid; r < p.requests; r += kPlanThreads)
-        if (p.starts[r + 1] < 0) p.starts[r + 1] = (int)rows_used;
+        if (p.starts[r + 1] < 0) {
+            p.starts[r + 1] = (int)rows_used;
+            p.block_starts[r + 1] = (int)blocks_used;
+        }
     if (a.slots) {
         // a slot named twice belongs to the first request with tokens
         for (int r = r0; r < r1; r++)

@@ -14,14 +14,14 @@ constexpr int kBlockTokens = 64;  // STEPQ_BLOCK
 constexpr int kF32 = 0, kF16 = 1, kBF16 = 2;         // STEPQ_F32 ...
 constexpr int kGdn = 0, kKda = 1, kLinear = 2;       // STEPQ_GDN ...
 // bits of a plan's status word (STEPQ_PLAN_*)
-constexpr int kPlanBadLength = 1, kPlanTooMany = 2, kPlanBadSlot = 4, kPlanSlotTwice = 8, kPlanNoSlot = 16;
+constexpr int kPlanBadLength = 1, kPlanTooMany = 2, kPlanBadSlot = 4, kPlanSlotTwice = 8, kPlanNoSlot = 16, kPlanTimeout = 32;
 
 // The arrays of a plan's buffer (stepq_plan_regions).
 struct PlanView {
     int requests, tokens, slots, blocks;  // capacity
     int *starts, *slot, *live, *fresh;
     int *token_request, *token_position;
-    int *block_request, *block_first;
+    int *block_starts, *block_request, *block_first;
     int *head;
     int *owner, *list;  // scratch: [slots] the request that names a slot, [requests] free slots
 };
@@ -48,6 +48,9 @@ struct PromptArgs {
 };
 // The recurrence token by token (any length; meant for a few tokens a request).
 cudaError_t launch_prompt_steps(const PromptArgs &a, cudaStream_t s);
+// The recurrence in blocks of tokens, and the scratch that takes.
+size_t prompt_scratch_bytes(const PromptArgs &a);
+cudaError_t launch_prompt_blocks(const PromptArgs &a, cudaStream_t s);
 
 struct BeamArgs {
     int groups, beams, vocab, n, dtype;

@@ -16,7 +16,7 @@ static_assert(STEPQ_F32 == stepq::kF32 && STEPQ_F16 == stepq::kF16 && STEPQ_BF16
 static_assert(STEPQ_GDN == stepq::kGdn && STEPQ_KDA == stepq::kKda && STEPQ_LINEAR == stepq::kLinear, "variants");
 static_assert(STEPQ_PLAN_BAD_LENGTH == stepq::kPlanBadLength && STEPQ_PLAN_TOO_MANY == stepq::kPlanTooMany &&
                   STEPQ_PLAN_BAD_SLOT == stepq::kPlanBadSlot && STEPQ_PLAN_SLOT_TWICE == stepq::kPlanSlotTwice &&
-                  STEPQ_PLAN_NO_SLOT == stepq::kPlanNoSlot,
+                  STEPQ_PLAN_NO_SLOT == stepq::kPlanNoSlot && STEPQ_PLAN_TIMEOUT == stepq::kPlanTimeout,
               "status bits");
 
 namespace {
@@ -57,6 +57,7 @@ stepq_status plan_regions(const stepq_plan_desc *d, stepq_plan_regions *r)
     r->fresh = o;          o = up(o + 4 * R, 16);
     r->token_request = o;  o = up(o + 4 * T, 16);
     r->token_position = o; o = up(o + 4 * T, 16);
+    r->block_starts = o;   o = up(o + 4 * (R + 1), 16);
     r->block_request = o;  o = up(o + 4 * (size_t)r->blocks, 16);
     r->block_first = o;    o = up(o + 4 * (size_t)r->blocks, 16);
     r->scratch = o;        o = up(o + 4 * ((size_t)d->slots + R), 16);
@@ -85,6 +86,7 @@ stepq_status plan_view(const stepq_plan_desc *d, const void *plan, size_t bytes,
     v->fresh = at(r.fresh);
     v->token_request = at(r.token_request);
     v->token_position = at(r.token_position);
+    v->block_starts = at(r.block_starts);
     v->block_request = at(r.block_request);
     v->block_first = at(r.block_first);
     v->owner = at(r.scratch);
@@ -187,6 +189,8 @@ stepq_status stepq_plan_check(const stepq_plan_desc *desc, const void *plan, siz
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return cuda_fail(e, "stepq_plan_check read");
     if (bits == 0) return STEPQ_OK;
+    if (bits & STEPQ_PLAN_TIMEOUT)
+        return fail(STEPQ_ERR_CUDA, "a prompt kernel gave up waiting for a copy; its requests' states and rows are not valid");
     std::string why;
     if (bits & STEPQ_PLAN_BAD_LENGTH) why += "; a length below 0 or above max_length";
     if (bits & STEPQ_PLAN_TOO_MANY) why += "; more tokens than the plan's capacity";
@@ -199,7 +203,15 @@ stepq_status stepq_plan_check(const stepq_plan_desc *desc, const void *plan, siz
 size_t stepq_prompt_scratch_bytes(const stepq_plan_desc *plan_desc, const stepq_prompt_desc *desc)
 {
     if (check_prompt_desc(plan_desc, desc) != STEPQ_OK) return (size_t)-1;
-    return 0;
+    if (plan_desc->requests == 0 || plan_desc->tokens == 0 || desc->max_length <= STEPQ_STEP_TOKENS) return 0;
+    stepq::PromptArgs a{};
+    a.p.requests = plan_desc->requests;
+    a.p.blocks = plan_desc->tokens / STEPQ_BLOCK + plan_desc->requests;
+    a.variant = desc->variant;
+    a.dtype = desc->dtype;
+    a.heads = desc->heads;
+    a.share = desc->heads / desc->heads_qk;
+    return stepq::prompt_scratch_bytes(a);
 }
 
 stepq_status stepq_prompt(const stepq_plan_desc *plan_desc, const void *plan, size_t plan_bytes,
@@ -261,7 +273,8 @@ stepq_status stepq_prompt(const stepq_plan_desc *plan_desc, const void *plan, si
     a.S = S;
     a.out = out;
     a.scratch = static_cast<uint8_t *>(scratch);
-    cudaError_t err = stepq::launch_prompt_steps(a, static_cast<cudaStream_t>(cuda_stream));
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    cudaError_t err = desc->max_length <= STEPQ_STEP_TOKENS ? stepq::launch_prompt_steps(a, s) : stepq::launch_prompt_blocks(a, s);
     return err == cudaSuccess ? STEPQ_OK : cuda_fail(err, "stepq_prompt launch");
 }
 

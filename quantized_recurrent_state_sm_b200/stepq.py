@@ -63,7 +63,7 @@ class PlanDesc(C.Structure):
 
 class PlanRegions(C.Structure):
     _fields_ = [(f, C.c_size_t) for f in ("starts", "slot", "live", "fresh", "token_request", "token_position",
-                                          "block_request", "block_first", "head", "scratch", "total")] + [("blocks", C.c_int)]
+                                          "block_starts", "block_request", "block_first", "head", "scratch", "total")] + [("blocks", C.c_int)]
 
 
 class PromptDesc(C.Structure):
@@ -414,7 +414,7 @@ class RequestPlan:
 
     Holds room for `requests` requests with `tokens` token rows in all, whose
     states live in `slots` slots (default: one each).  After build() the int32
-    views starts [requests + 1], slots and live [requests], fresh [requests],
+    views starts and block_starts [requests + 1], slots and live [requests], fresh [requests],
     token_request and token_position [tokens], block_request and block_first
     [blocks] describe the batch (include/stepq.h, stepq_plan_regions).
     """
@@ -435,7 +435,7 @@ class RequestPlan:
             return ints[offset // 4: offset // 4 + n]
 
         self.head = view(r.head, 4)
-        self.starts = view(r.starts, self.requests + 1)
+        self.starts, self.block_starts = (view(o, self.requests + 1) for o in (r.starts, r.block_starts))
         self.slots, self.live, self.fresh = (view(o, self.requests) for o in (r.slot, r.live, r.fresh))
         self.token_request, self.token_position = (view(o, self.tokens) for o in (r.token_request, r.token_position))
         self.block_request, self.block_first = (view(o, self.blocks) for o in (r.block_request, r.block_first))

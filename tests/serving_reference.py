@@ -13,7 +13,7 @@ def plan(requests, tokens, n_slots, lengths, contexts=None, slots=None, busy=Non
     max_length = tokens if max_length is None else max_length
     contexts = contexts or [0] * n
     busy = None if busy is None else list(busy)
-    p = dict(starts=[0], slots=[-1] * requests, live=[-1] * requests, fresh=[0] * requests, token_request=[-1] * tokens,
+    p = dict(starts=[0], block_starts=[0], slots=[-1] * requests, live=[-1] * requests, fresh=[0] * requests, token_request=[-1] * tokens,
              token_position=[-1] * tokens, block_request=[], block_first=[], status=0)
     over = False
     used = 0
@@ -38,6 +38,7 @@ def plan(requests, tokens, n_slots, lengths, contexts=None, slots=None, busy=Non
             p["block_first"].append(b)
         used += ln
         p["starts"].append(used)
+        p["block_starts"].append(len(p["block_first"]))
         p["fresh"][r] = int(contexts[r] == 0)
         s = r if slots is None else slots[r]
         good = 0 <= s < n_slots
@@ -68,6 +69,7 @@ def plan(requests, tokens, n_slots, lengths, contexts=None, slots=None, busy=Non
                 busy[free] = 1
                 p["live"][r] = p["slots"][r] = free
     p["starts"] += [used] * (requests - n)
+    p["block_starts"] += [len(p["block_first"])] * (requests - n)
     blocks = tokens // BLOCK + requests
     for f in ("block_request", "block_first"):
         p["head_blocks"] = len(p[f])

@@ -53,7 +53,7 @@ def test_plan_layout(S):
     assert S.lib.stepq_plan_layout(C.byref(d), C.byref(r)) == 0
     assert r.blocks == 130 // 64 + 5 and S.lib.stepq_plan_bytes(C.byref(d)) == r.total
     order = [(r.head, 16), (r.starts, 24), (r.slot, 20), (r.live, 20), (r.fresh, 20), (r.token_request, 520),
-             (r.token_position, 520), (r.block_request, 4 * r.blocks), (r.block_first, 4 * r.blocks), (r.scratch, 4 * 14)]
+             (r.token_position, 520), (r.block_starts, 24), (r.block_request, 4 * r.blocks), (r.block_first, 4 * r.blocks), (r.scratch, 4 * 14)]
     end = 0
     for at, n in order:
         assert at >= end and at % 16 == 0
@@ -130,7 +130,7 @@ def check_plan(S, requests, tokens, n_slots, lengths, contexts=None, slots=None,
     p.buffer.fill_(0xA5)
     b = None if busy is None else torch.tensor(busy, dtype=torch.uint8, device="cuda")
     p.build(i32(lengths), None if contexts is None else i32(contexts), None if slots is None else i32(slots), b, max_length)
-    for f in ("starts", "slots", "live", "fresh", "token_request", "token_position", "block_request", "block_first", "head"):
+    for f in ("starts", "block_starts", "slots", "live", "fresh", "token_request", "token_position", "block_request", "block_first", "head"):
         assert getattr(p, f).tolist() == want[f], f
     if busy is not None:
         assert b.tolist() == want["busy"]
