@@ -15,7 +15,7 @@ namespace dev {
 __device__ __forceinline__ void mma16816(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -34,6 +34,20 @@ __device__ __forceinline__ void ldsm4_t(uint32_t *r, uint32_t addr)
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
+}
+
+// The same into two right operands of two registers each.
+__device__ __forceinline__ void ldsm4(uint32_t *p, uint32_t *q, uint32_t addr)
+{
+    uint32_t r[4];
+    ldsm4(r, addr);
+    p[0] = r[0]; p[1] = r[1]; q[0] = r[2]; q[1] = r[3];
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t *p, uint32_t *q, uint32_t addr)
+{
+    uint32_t r[4];
+    ldsm4_t(r, addr);
+    p[0] = r[0]; p[1] = r[1]; q[0] = r[2]; q[1] = r[3];
 }
 
 // Powers of two that bring a row whose largest magnitude is m near 2^13, and
@@ -55,13 +69,14 @@ __device__ __forceinline__ uint32_t pack_half(float x, float y)
 }
 
 // hi and lo halves of two scaled numbers.
-__device__ __forceinline__ void split_half(float x, float y, uint32_t *hi, uint32_t *lo)
+__device__ __forceinline__ void split_half(float2 x, uint32_t *hi, uint32_t *lo)
 {
-    const __half2 h = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(h);
+    const __half2 h = __float22half2_rn(x);
+    const float2 d = __ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), x);
     *hi = *reinterpret_cast<const uint32_t *>(&h);
-    *lo = pack_half(x - f.x, y - f.y);
+    *lo = pack_half(d.x, d.y);
 }
+__device__ __forceinline__ void split_half(float x, float y, uint32_t *hi, uint32_t *lo) { split_half(make_float2(x, y), hi, lo); }
 
 }  // namespace dev
 }  // namespace stepq

@@ -23,6 +23,7 @@
 #include "stepq_device.cuh"
 #include "stepq_mma.cuh"
 #include "stepq_serve.cuh"
+#include "stepq_tcgen05.cuh"
 
 namespace stepq {
 namespace {
@@ -41,11 +42,12 @@ constexpr int kStateFloats = 4 * kC + kDK;
 constexpr int kOutFloats = 2 * kC;          // for the output: unscale of the Q rows times c_t, of the P rows
 constexpr long long kWaitLimit = 1LL << 32;  // cycles, about two seconds
 
-// Byte of element (row, col) of an operand tile: 16-byte chunks of a row are
-// permuted by the row, so that eight rows of one column block lie in different
-// banks.
-__device__ __forceinline__ int tile_at(int row, int col) { return row * 256 + ((((col >> 3) ^ row) & 7) | (col >> 3 & 8)) * 16 + (col & 7) * 2; }
+// Byte of element (row, col) of an operand tile [64][128] (two halves of 64
+// columns) and of a [64][64] one: rows of 128 bytes whose 16-byte chunks are
+// permuted by the row, the layout the tensor cores read and in which eight rows
+// of one chunk lie in different banks.
 __device__ __forceinline__ int square_at(int row, int col) { return row * 128 + (((col >> 3) ^ row) & 7) * 16 + (col & 7) * 2; }
+__device__ __forceinline__ int tile_at(int row, int col) { return (col >> 6) * (kTileBytes / 2) + square_at(row, col & 63); }
 
 // The scratch of a launch over `blocks` blocks.
 struct Scratch {
@@ -133,21 +135,25 @@ __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, con
         uint32_t ah[4], al[4];
         ldsm4(ah, a0 + tile_at(arow, 16 * i + acol));
         if (NP == 2) ldsm4(al, a0 + kTileBytes + tile_at(arow, 16 * i + acol));
+        uint32_t b[kC / 8][2];
 #pragma unroll
-        for (int j = 0; j < kC / 8; j += 2) {
-            if (j >= tiles) continue;
-            uint32_t bh[4], bl[4];
-            ldsm4(bh, b0 + tile_at(8 * j + brow, 16 * i + bcol));
-            if (NP == 2) {
-                ldsm4(bl, b0 + kTileBytes + tile_at(8 * j + brow, 16 * i + bcol));
+        for (int j = 0; j < kC / 8; j += 2)
+            if (j < tiles) ldsm4(b[j], b[j + 1], b0 + tile_at(8 * j + brow, 16 * i + bcol));
+        if (NP == 2) {
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    mma16816(acc[j + e], al[0], al[1], al[2], al[3], bh[2 * e], bh[2 * e + 1]);
-                    mma16816(acc[j + e], ah[0], ah[1], ah[2], ah[3], bl[2 * e], bl[2 * e + 1]);
-                }
-            }
+            for (int j = 0; j < kC / 8; j++)
+                if (j < tiles) mma16816(acc[j], al[0], al[1], al[2], al[3], b[j][0], b[j][1]);
+        }
 #pragma unroll
-            for (int e = 0; e < 2; e++) mma16816(acc[j + e], ah[0], ah[1], ah[2], ah[3], bh[2 * e], bh[2 * e + 1]);
+        for (int j = 0; j < kC / 8; j++)
+            if (j < tiles) mma16816(acc[j], ah[0], ah[1], ah[2], ah[3], b[j][0], b[j][1]);
+        if (NP == 2) {
+#pragma unroll
+            for (int j = 0; j < kC / 8; j += 2)
+                if (j < tiles) ldsm4(b[j], b[j + 1], b0 + kTileBytes + tile_at(8 * j + brow, 16 * i + bcol));
+#pragma unroll
+            for (int j = 0; j < kC / 8; j++)
+                if (j < tiles) mma16816(acc[j], ah[0], ah[1], ah[2], ah[3], b[j][0], b[j][1]);
         }
     }
 }
@@ -264,7 +270,7 @@ __device__ __forceinline__ bool find_block(const PromptArgs &a, int first_block,
 template <class T, int V, int NP>
 __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_block, Scratch sc)
 {
-    extern __shared__ __align__(128) char smem[];
+    extern __shared__ __align__(1024) char smem[];
     __shared__ float ek[kC], eq[kC], s_alpha[kC], s_beta[kC], s_inv[kC], s_p[kC];
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
     const int heads_k = a.heads / a.share;
@@ -372,469 +378,462 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
 }
 
 // ---------------------------------------------------------------------------
-// The walk over a request's blocks.  The state is held transposed: a state warp
-// owns 16 value columns x 128 key rows as fp32 accumulators, whose register
-// layout is also the layout of a product's left operand, so state, U and the
-// state's update pass from product to product without leaving the registers.
-// A second warp beside each state warp makes the output from the same halves,
-// off the chain from block to block.  Operand tiles come by bulk copies.
+// The walk over a request's blocks: one CTA a state, all products on the
+// fifth-generation tensor cores.  Everything is held transposed, value columns
+// as the 128 lanes of tensor memory, so that each product's result, read from
+// tensor memory by the threads of its lanes, scaled and split, goes back there
+// as the next product's left operand:
+//   Y = S^T K^T  ->  R = beta (V^T - Y)  ->  U = R inv^T  ->  S^T <- keep S^T + U' K,
+//   out^T = S^T Q^T + U P^T.
+// Warps 0-7 keep the state (64 key rows of one value column a thread) and walk
+// this chain; warps 8-11 finish the output, off the chain; warp 12 issues the
+// products and the copies of the operands, warp 13 copies V.  Sums in tensor memory never pass
+// from block to block: the state is updated in registers, rounded to nearest.
 // ---------------------------------------------------------------------------
-enum { kPartK, kPartInv, kPartQ, kPartP, kPartK2, kParts };
+constexpr int kStateWarps = 8, kOutWarps = 4;
+constexpr int kIssueWarp = kStateWarps + kOutWarps, kValueWarp = kIssueWarp + 1;
+constexpr int kWalkThreads = 32 * (kValueWarp + 1);
+// columns of tensor memory: Y, then the halves of R, then of U'; S^T Q^T; U,
+// then its halves; U P^T; the state's update; the halves of S
+constexpr int kColY = 0, kColSQ = 64, kColU = 128, kColUP = 192, kColD = 256, kColS = 384, kColumns = 512;
 
-template <class T, int V, int NP, int NR>
+template <class T, int V, int NP>
 struct Walk {
-    static constexpr int kKStages = V == kKda ? 1 : 2;  // K is read again at the block's end
-    static constexpr int kThreads = 32 * 2 * NR;  // no copying warp: a ninth warp would cost the others a third of their registers
+    // K is read again at the block's end, so that two lie side by side, except
+    // with a gate per key row, which has other rows there; two Q (and the
+    // output's scales), for the output may lag behind
+    static constexpr int kKStages = V == kKda ? 1 : 2;
     static constexpr int kKBytes = NP * kTileBytes;
-    static constexpr int kInvBytes = (V == kLinear ? 0 : kSquareBytes) + kStateFloats * 4;
-    static constexpr int kPBytes = kSquareBytes + kOutFloats * 4;
-    static constexpr int kVRow = sizeof(T) == 4 ? 80 : 48;  // bytes of a V row in shared memory (16 columns and a pad)
-    // exchange of a state warp with its output warp: halves of S (8 k-steps x 2 x 512), of U (4 x 2 x 512), unscales
-    static constexpr int kXBytes = 8192 + 4096 + 128;
+    static constexpr int kVRow = kDV * sizeof(T);
     static constexpr int oK = 0;
-    static constexpr int oInv = oK + kKStages * kKBytes;
-    static constexpr int oQ = oInv + kInvBytes;
-    static constexpr int oP = oQ + kKBytes;
-    static constexpr int oK2 = oP + kPBytes;
-    static constexpr int oX = oK2 + (V == kKda ? kKBytes : 0);
-    static constexpr int oV = oX + NR * kXBytes;
-    static constexpr int oBar = oV + NR * 2 * kC * kVRow;
-    static constexpr int kBars = kParts + 1 + 4 * NR;
-    static constexpr int oCount = oBar + 8 * kBars;
-    static constexpr int kBytes = oCount + 4 * (kParts + 1);
+    static constexpr int oQ = oK + kKStages * kKBytes;
+    static constexpr int oK2 = oQ + 2 * kKBytes;
+    static constexpr int oInv = oK2 + (V == kKda ? kKBytes : 0);
+    static constexpr int oP = oInv + (V == kLinear ? 0 : kSquareBytes);
+    static constexpr int oV = oP + kSquareBytes;
+    static constexpr int oSv = oV + kC * kVRow;
+    static constexpr int oOv = oSv + 2 * kStateFloats * 4;
+    static constexpr int oMax = oOv + 2 * kOutFloats * 4;   // [3][2][128] row maxima of the two halves of the state warps
+    static constexpr int oBack = oMax + 3 * 2 * kDV * 4;    // [2][2][128] unscales of S and U
+    static constexpr int oBar = oBack + 2 * 2 * kDV * 4;
+    static constexpr int oFlags = oBar + 8 * 32;            // tensor memory address; whether a wait gave up
+    static constexpr int kBytes = oFlags + 8;
     static_assert(kBytes <= 227 * 1024, "shared memory of a CTA");
 };
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
+// Barriers.  Copies: K (2), Q with the output's scales (2), K2, the inverse, P,
+// V, the state's scales (2).  Products done: Y, S^T Q^T, U, U P^T, update.
+// Halves written: S, R, U.  Output read: S^T Q^T, U P^T.
+enum { kFullK = 0, kFullQ = 2, kFullK2 = 4, kFullInv, kFullP, kFullV, kFullSv, kDoneY = 10, kDoneSQ, kDoneU, kDoneUP, kDoneD, kGotS, kGotR, kGotU, kReadSQ, kReadUP, kBarriers };
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dev::smem_addr(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dev::smem_addr(dst)), "l"(src) : "memory");
 }
 
-// Maximum over the four lanes that share a row of an accumulator.
-__device__ __forceinline__ float quad_max(float m)
-{
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-    return fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-}
-
-// An accumulator of N column tiles as the halves of a left operand; the rows'
-// unscales in back0 (row g) and back1 (row g + 8).
+// Row maxima of the two halves of the state warps, exchanged: scale and unscale
+// of N rows (one a thread), in one meeting of the 256 threads.
 template <int N>
-__device__ __forceinline__ void split_rows(const float (*x)[4], uint32_t (*hi)[4], uint32_t (*lo)[4], float *back0, float *back1)
+__device__ __forceinline__ void meet(float *sm, int half, int lane, const float *m, float *scale, float *back)
 {
-    float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-    for (int j = 0; j < N; j++) {
-        m0 = fmaxf(m0, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
-        m1 = fmaxf(m1, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+    for (int i = 0; i < N; i++) sm[(2 * i + half) * kDV + lane] = m[i];
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i++) dev::row_scale(fmaxf(m[i], sm[(2 * i + (half ^ 1)) * kDV + lane]), &scale[i], &back[i]);
+}
+
+// N pairs x(i) of a row's numbers, times its scale, as halves into tensor memory.
+template <int N, class F>
+__device__ __forceinline__ void store_halves(uint32_t hi_at, uint32_t lo_at, float scale, const F &x)
+{
+    const float2 sc = make_float2(scale, scale);
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) dev::split_half(__fmul2_rn(x(i + j), sc), &hi[j], &lo[j]);
+        tc::st8(hi_at + i, hi);
+        tc::st8(lo_at + i, lo);
     }
-    float s0, s1;
-    dev::row_scale(quad_max(m0), &s0, back0);
-    dev::row_scale(quad_max(m1), &s1, back1);
-#pragma unroll
-    for (int i = 0; i < N / 2; i++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            dev::split_half(x[2 * i + e][0] * s0, x[2 * i + e][1] * s0, &hi[i][2 * e], &lo[i][2 * e]);
-            dev::split_half(x[2 * i + e][2] * s1, x[2 * i + e][3] * s1, &hi[i][2 * e + 1], &lo[i][2 * e + 1]);
-        }
 }
 
-__device__ __forceinline__ void v_pair(const char *tile, int row, int col, float *x, float)
-{
-    x[0] = *reinterpret_cast<const float *>(tile + row * 80 + col * 4);
-    x[1] = *reinterpret_cast<const float *>(tile + (row + 1) * 80 + col * 4);
-}
+// The larger of m and the magnitudes of a pair.
+__device__ __forceinline__ float max_abs(float m, float2 x) { return fmaxf(fmaxf(m, fabsf(x.x)), fabsf(x.y)); }
 
-template <class T, int V, int NP, int NR>
-__global__ void __launch_bounds__(Walk<T, V, NP, NR>::kThreads, 1) k_block_walk(PromptArgs a, int first_block, int n_blocks, Scratch sc)
+__device__ __forceinline__ float2 pair_at(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+
+template <class T>
+__device__ __forceinline__ float v_at(const char *row, int i);
+template <>
+__device__ __forceinline__ float v_at<float>(const char *row, int i) { return reinterpret_cast<const float *>(row)[i]; }
+template <>
+__device__ __forceinline__ float v_at<__half>(const char *row, int i) { return __half2float(reinterpret_cast<const __half *>(row)[i]); }
+template <>
+__device__ __forceinline__ float v_at<__nv_bfloat16>(const char *row, int i) { return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(row)[i]); }
+
+template <class T>
+__device__ __forceinline__ T to_t(float x);
+template <>
+__device__ __forceinline__ float to_t<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half to_t<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 to_t<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+template <class T, int V, int NP>
+__global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, int first_block, int n_blocks, Scratch sc)
 {
-    using W = Walk<T, V, NP, NR>;
-    extern __shared__ __align__(128) char smem[];
-    // a barrier and a counter for each part (K has two stages, the second last), four barriers a pair of warps
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + W::oBar), *xbar = full + kParts + 1;
-    unsigned *used = reinterpret_cast<unsigned *>(smem + W::oCount);
-    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
-    constexpr int slices = kDV / (16 * NR);
-    const int slice = blockIdx.x % slices, item = blockIdx.x / slices;
-    const int r = item / a.heads, h = item - r * a.heads;
+    using W = Walk<T, V, NP>;
+    // no other shared memory, so that it starts at an aligned address the compiler knows
+    extern __shared__ __align__(1024) char smem[];
+    volatile int *s_dead = reinterpret_cast<volatile int *>(smem + W::oFlags + 4);
+    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
+    const int r = blockIdx.x / a.heads, h = blockIdx.x - r * a.heads;
     const int live = a.p.live[r];
     if (live < 0) return;
     // the request's blocks of this launch
     const int all0 = a.p.block_starts[r], b0 = max(all0, first_block), b1 = min(a.p.block_starts[r + 1], first_block + n_blocks);
     if (b0 >= b1) return;
-    const int row0 = a.p.starts[r], row_end = a.p.starts[r + 1];
+    const int row0 = a.p.starts[r] + (b0 - all0) * kC, row_end = a.p.starts[r + 1], count = b1 - b0;
+    uint64_t *bar = reinterpret_cast<uint64_t *>(smem + W::oBar);
+    if (w == kIssueWarp) tc::alloc(reinterpret_cast<uint32_t *>(smem + W::oFlags), kColumns);
     if (tid == 0) {
-        for (int i = 0; i <= kParts; i++) {
-            dev::mbar_init(&full[i], 1);
-            used[i] = 0;
-        }
-        for (int i = 0; i < 4 * NR; i++) dev::mbar_init(&xbar[i], 1);
+        // operands have to lie at multiples of 1024 bytes
+        *s_dead = (dev::smem_addr(smem) & 1023) != 0;
+        if (*s_dead) atomicOr(a.p.head, kPlanTimeout);
+        for (int i = 0; i < kBarriers; i++)
+            dev::mbar_init(&bar[i], i == kGotS || i == kGotR || i == kGotU ? kStateWarps : (i == kReadSQ || i == kReadUP ? kOutWarps : (i == kFullV ? 32 : 1)));
         dev::fence_barrier_init();
     }
+    // rows of V behind the request's last are multiplied by zero: they must be finite
+    for (int i = tid; i < kC * W::kVRow / 16; i += kWalkThreads) *reinterpret_cast<uint4 *>(smem + W::oV + 16 * i) = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc::fence_before();
     __syncthreads();
-    const int count = b1 - b0;
-    int *status = a.p.head;
-    auto wait = [&](uint64_t *bar, int parity) -> bool {
-        if (dev::mbar_wait_bounded(bar, (uint32_t)parity, kWaitLimit)) return true;
-        atomicOr(status, kPlanTimeout);
-        return false;
+    tc::fence_after();
+    constexpr uint32_t tm = 0;  // all columns are this CTA's: they start at 0
+    // Bounded: a wait that gives up marks the CTA dead, and nothing waits any
+    // more; every thread runs to the end.
+    auto wait = [&](int i, int parity) {
+        if (dev::mbar_try_wait(&bar[i], (uint32_t)parity)) return;
+        const long long t0 = clock64();
+        while (!*s_dead && !dev::mbar_try_wait(&bar[i], (uint32_t)parity))
+            if (clock64() - t0 > kWaitLimit) {
+                *s_dead = 1;
+                atomicOr(a.p.head, kPlanTimeout);
+            }
     };
-    // the copies of a part of the request's it-th block (one thread)
-    auto copy = [&](int part, int it) {
-        const int heads_k = V == kKda ? a.heads : a.heads / a.share, hk = V == kKda ? h : h / a.share;
-        const size_t b = (size_t)(b0 - first_block + it);
-        const size_t tile = (b * heads_k + hk) * W::kKBytes, bh = b * a.heads + h;
-        const int stage = part == kPartK ? it % W::kKStages : 0;
-        uint64_t *f = &full[stage ? kParts : part];
-        const uint8_t *src = a.scratch;
-        if (part == kPartInv) {
-            dev::mbar_arrive_expect_tx(f, W::kInvBytes);
-            if (V != kLinear) dev::bulk_g2s(smem + W::oInv, src + sc.inv + bh * kSquareBytes, kSquareBytes, f);
-            dev::bulk_g2s(smem + W::oInv + W::kInvBytes - kStateFloats * 4, src + sc.sv + bh * kStateFloats * 4, kStateFloats * 4, f);
-        } else if (part == kPartP) {
-            dev::mbar_arrive_expect_tx(f, W::kPBytes);
-            dev::bulk_g2s(smem + W::oP, src + sc.p + bh * kSquareBytes, kSquareBytes, f);
-            dev::bulk_g2s(smem + W::oP + kSquareBytes, src + sc.ov + bh * kOutFloats * 4, kOutFloats * 4, f);
-        } else {
-            const int dst = part == kPartK ? W::oK + stage * W::kKBytes : (part == kPartQ ? W::oQ : W::oK2);
-            dev::mbar_arrive_expect_tx(f, W::kKBytes);
-            dev::bulk_g2s(smem + dst, src + (part == kPartK ? sc.k : (part == kPartQ ? sc.q : sc.k2)) + tile, W::kKBytes, f);
-        }
-    };
-    // A warp is done with a part of block it: the last of the NR warps that read
-    // it has the next block's copied into its place.
-    auto release = [&](int part, int it) {
+    auto arrive = [&](int i) {
         __syncwarp();
-        if (l == 0) {
-            const int stages = part == kPartK ? W::kKStages : 1;
-            unsigned *n = &used[part == kPartK && it % W::kKStages ? kParts : part], old;
-            asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(old) : "r"(dev::smem_addr(n)) : "memory");
-            if (old % NR == NR - 1 && it + stages < count) copy(part, it + stages);
-        }
+        if (l == 0) dev::mbar_arrive(&bar[i]);
     };
-    if (tid == 0) {
-        copy(kPartK, 0);
-        copy(kPartInv, 0);
-        copy(kPartQ, 0);
-        copy(kPartP, 0);
-        if (V == kKda) copy(kPartK2, 0);
-        if (W::kKStages == 2 && count > 1) copy(kPartK, 1);
-    }
+    const float *sv_all = reinterpret_cast<const float *>(smem + W::oSv), *ov_all = reinterpret_cast<const float *>(smem + W::oOv);
+    float *s_max = reinterpret_cast<float *>(smem + W::oMax), *s_back = reinterpret_cast<float *>(smem + W::oBack);
 
-    const bool out_warp = w >= NR;
-    const int wr = out_warp ? w - NR : w;  // row group of the CTA
-    const int col0 = slice * 16 * NR + 16 * wr;  // its 16 value columns
-    uint64_t *sfull = &xbar[4 * wr], *sempty = sfull + 1, *ufull = sfull + 2, *uempty = sfull + 3;
-    char *xs = smem + W::oX + wr * W::kXBytes, *xu = xs + 8192;
-    float *xback = reinterpret_cast<float *>(xs + 8192 + 4096);  // unscales of S [16] and of U [16]
-    const int arow = (l & 7) + ((l >> 3) & 1) * 8, acol = (l >> 4) * 8;  // ldmatrix: rows of a left operand
-    const int brow = (l & 7) + (l >> 4) * 8, bcol = ((l >> 3) & 1) * 8;  // two column tiles of a right operand
-
-    if (out_warp) {
-        // ---- output: rows are tokens ----
-        const uint32_t q0 = dev::smem_addr(smem + W::oQ), p0 = dev::smem_addr(smem + W::oP);
-        const float *ov = reinterpret_cast<const float *>(smem + W::oP + kSquareBytes);
-        T *out = static_cast<T *>(a.out);
+    if (w == kValueWarp) {
+        // ---- V: rows of the request's tokens, as 16-byte copies of all lanes (a bulk copy a row would cost its issue, 64 times) ----
+        const T *vg = static_cast<const T *>(a.v) + h * kDV;
+        constexpr int pieces = W::kVRow / 16;
         for (int it = 0; it < count; it++) {
-            const int par = it & 1, t0 = row0 + (b0 - all0 + it) * kC, n = min(kC, row_end - t0), nm = (n + 15) / 16;
-            uint32_t hi[8][4], lo[8][4];
-            if (!wait(sfull, par)) return;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(xs + (2 * i) * 512 + l * 16), y = *reinterpret_cast<const uint4 *>(xs + (2 * i + 1) * 512 + l * 16);
-                hi[i][0] = x.x; hi[i][1] = x.y; hi[i][2] = x.z; hi[i][3] = x.w;
-                lo[i][0] = y.x; lo[i][1] = y.y; lo[i][2] = y.z; lo[i][3] = y.w;
-            }
-            float sb[2][2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) { sb[e][0] = xback[8 * e + 2 * c]; sb[e][1] = xback[8 * e + 2 * c + 1]; }
-            __syncwarp();
-            if (l == 0) dev::mbar_arrive(sempty);
-            if (!wait(&full[kPartQ], par)) return;
-            float o[4][2][4] = {};
-#pragma unroll
-            for (int i = 0; i < 8; i++)
-#pragma unroll
-                for (int m = 0; m < 4; m++) {
-                    if (m >= nm) continue;
-                    uint32_t x[4];
-                    ldsm4(x, q0 + tile_at(16 * m + arow, 16 * i + acol));
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        mma16816(o[m][e], x[0], x[1], x[2], x[3], lo[i][e], lo[i][2 + e]);
-                        mma16816(o[m][e], x[0], x[1], x[2], x[3], hi[i][e], hi[i][2 + e]);
-                    }
-                    if (NP == 2) {
-                        ldsm4(x, q0 + kTileBytes + tile_at(16 * m + arow, 16 * i + acol));
-#pragma unroll
-                        for (int e = 0; e < 2; e++) mma16816(o[m][e], x[0], x[1], x[2], x[3], hi[i][e], hi[i][2 + e]);
-                    }
-                }
-            release(kPartQ, it);
-            if (!wait(ufull, par)) return;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(xu + (2 * i) * 512 + l * 16), y = *reinterpret_cast<const uint4 *>(xu + (2 * i + 1) * 512 + l * 16);
-                hi[i][0] = x.x; hi[i][1] = x.y; hi[i][2] = x.z; hi[i][3] = x.w;
-                lo[i][0] = y.x; lo[i][1] = y.y; lo[i][2] = y.z; lo[i][3] = y.w;
-            }
-            float ub[2][2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) { ub[e][0] = xback[16 + 8 * e + 2 * c]; ub[e][1] = xback[16 + 8 * e + 2 * c + 1]; }
-            __syncwarp();
-            if (l == 0) dev::mbar_arrive(uempty);
-            if (!wait(&full[kPartP], par)) return;
-#pragma unroll
-            for (int m = 0; m < 4; m++) {
-                if (m >= nm) continue;
-                float p[2][4] = {};
-#pragma unroll
-                for (int i = 0; i <= m; i++) {
-                    uint32_t x[4], y[4];
-                    ldsm4(x, p0 + square_at(16 * m + arow, 16 * i + acol));
-                    ldsm4(y, p0 + kSquareBytes / 2 + square_at(16 * m + arow, 16 * i + acol));
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        mma16816(p[e], x[0], x[1], x[2], x[3], lo[i][e], lo[i][2 + e]);
-                        mma16816(p[e], y[0], y[1], y[2], y[3], hi[i][e], hi[i][2 + e]);
-                        mma16816(p[e], x[0], x[1], x[2], x[3], hi[i][e], hi[i][2 + e]);
-                    }
-                }
-#pragma unroll
-                for (int d = 0; d < 2; d++) {
-                    const int t = 16 * m + g + 8 * d;
-                    if (t >= n) continue;
-                    const float fq = ov[t], fp = ov[kC + t];
-                    T *dst = out + ((long long)(t0 + t) * a.heads + h) * kDV + col0 + 2 * c;
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const float x = fmaf(o[m][e][2 * d], fq * sb[e][0], p[e][2 * d] * (fp * ub[e][0]));
-                        const float y = fmaf(o[m][e][2 * d + 1], fq * sb[e][1], p[e][2 * d + 1] * (fp * ub[e][1]));
-                        if constexpr (sizeof(T) == 4) {
-                            *reinterpret_cast<float2 *>(dst + 8 * e) = make_float2(x, y);
-                        } else if constexpr (std::is_same<T, __half>::value) {
-                            *reinterpret_cast<__half2 *>(dst + 8 * e) = __floats2half2_rn(x, y);
-                        } else {
-                            *reinterpret_cast<__nv_bfloat162 *>(dst + 8 * e) = __floats2bfloat162_rn(x, y);
-                        }
-                    }
-                }
-            }
-            release(kPartP, it);
+            const int t0 = row0 + it * kC, n = min(kC, row_end - t0);
+            if (it > 0) wait(V == kLinear ? kGotU : kGotR, (it - 1) & 1);  // the rows before are read
+            for (int i = l; i < n * pieces; i += 32)
+                cp_async16(smem + W::oV + i / pieces * W::kVRow + i % pieces * 16, vg + (long long)(t0 + i / pieces) * a.stride_v + i % pieces * (16 / (int)sizeof(T)));
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(dev::smem_addr(&bar[kFullV])) : "memory");
         }
-        return;
-    }
-
-    // ---- state: rows are value columns ----
-    float *Sp = a.S + ((long long)(a.by_slot ? live : r) * a.heads + h) * (kDK * kDV) + col0 + g;
-    float s[16][4];
-    const bool zero = a.p.fresh[r] != 0 && b0 == all0;
-#pragma unroll
-    for (int j = 0; j < 16; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) s[j][e] = zero ? 0.f : Sp[(8 * j + 2 * c + (e & 1)) * kDV + 8 * (e >> 1)];
-    char *vt = smem + W::oV + wr * 2 * kC * W::kVRow;
-    const T *vg = static_cast<const T *>(a.v) + h * kDV + col0;
-    auto fetch_v = [&](int it) {
-        const int t0 = row0 + (b0 - all0 + it) * kC;
-        char *dst = vt + (it & 1) * kC * W::kVRow;
-        constexpr int chunks = 16 * sizeof(T) / 16;  // 16-byte pieces of a row
-#pragma unroll
-        for (int i = 0; i < chunks * kC / 32; i++) {
-            const int x = i * 32 + l, row = x / chunks, part = x % chunks, t = t0 + row;
-            cp_async16(dst + row * W::kVRow + part * 16, vg + (long long)min(t, row_end - 1) * a.stride_v + part * (16 / (int)sizeof(T)), t < row_end);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    fetch_v(0);
-    const float *sv = reinterpret_cast<const float *>(smem + W::oInv + W::kInvBytes - kStateFloats * 4);
-    const uint32_t inv0 = dev::smem_addr(smem + W::oInv);
-    for (int it = 0; it < count; it++) {
-        const int par = it & 1, t0 = row0 + (b0 - all0 + it) * kC, nk = (min(kC, row_end - t0) + 15) / 16;
-        const int stage = it % W::kKStages, kpar = (it / W::kKStages) & 1;
-        uint64_t *kfull = &full[stage ? kParts : kPartK];
-        const uint32_t k0 = dev::smem_addr(smem + W::oK + stage * W::kKBytes);
-        if (it + 1 < count) {
-            fetch_v(it + 1);
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-        } else {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-        }
-        __syncwarp();
-        float y[8][4] = {};
-        float sb0, sb1;
-        {
-            uint32_t hi[8][4], lo[8][4];
-            split_rows<16>(s, hi, lo, &sb0, &sb1);
-            // the output warp has taken the halves of the block before
-            if (!wait(sempty, par ^ 1)) return;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                *reinterpret_cast<uint4 *>(xs + (2 * i) * 512 + l * 16) = make_uint4(hi[i][0], hi[i][1], hi[i][2], hi[i][3]);
-                *reinterpret_cast<uint4 *>(xs + (2 * i + 1) * 512 + l * 16) = make_uint4(lo[i][0], lo[i][1], lo[i][2], lo[i][3]);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (w == kIssueWarp) {
+        // ---- products and copies ----
+        const int heads_k = V == kKda ? a.heads : a.heads / a.share, hk = V == kKda ? h : h / a.share;
+        const size_t first = (size_t)(b0 - first_block);
+        const uint8_t *src = a.scratch;
+        auto tile = [&](int it) { return ((first + it) * heads_k + hk) * (size_t)W::kKBytes; };
+        auto bh = [&](int it) { return (first + it) * a.heads + h; };
+        auto copy = [&](int b, int dst, size_t from, int bytes) {
+            if (tc::elect()) {
+                dev::mbar_arrive_expect_tx(&bar[b], bytes);
+                dev::bulk_g2s(smem + dst, src + from, bytes, &bar[b]);
             }
-            if (c == 0) { xback[g] = sb0; xback[g + 8] = sb1; }
-            __syncwarp();
-            if (l == 0) dev::mbar_arrive(sfull);
-            if (V != kLinear || it == 0)
-                if (!wait(kfull, kpar)) return;
+        };
+        auto copy_k = [&](int it) { copy(kFullK + it % W::kKStages, W::oK + it % W::kKStages * W::kKBytes, sc.k + tile(it), W::kKBytes); };
+        auto copy_q = [&](int it) {
+            if (tc::elect()) {
+                uint64_t *f = &bar[kFullQ + (it & 1)];
+                dev::mbar_arrive_expect_tx(f, W::kKBytes + kOutFloats * 4);
+                dev::bulk_g2s(smem + W::oQ + (it & 1) * W::kKBytes, src + sc.q + tile(it), W::kKBytes, f);
+                dev::bulk_g2s(smem + W::oOv + (it & 1) * kOutFloats * 4, src + sc.ov + bh(it) * kOutFloats * 4, kOutFloats * 4, f);
+            }
+        };
+        auto copy_sv = [&](int it) { copy(kFullSv + (it & 1), W::oSv + (it & 1) * kStateFloats * 4, sc.sv + bh(it) * kStateFloats * 4, kStateFloats * 4); };
+        copy_k(0);
+        copy_sv(0);
+        copy_q(0);
+        if (V == kKda) copy(kFullK2, W::oK2, sc.k2 + tile(0), W::kKBytes);
+        if (V != kLinear) copy(kFullInv, W::oInv, sc.inv + bh(0) * kSquareBytes, kSquareBytes);
+        copy(kFullP, W::oP, sc.p + bh(0) * kSquareBytes, kSquareBytes);
+        const uint32_t base = dev::smem_addr(smem);
+        // products of S^T with the rows of an operand tile
+        auto with_rows = [&](uint32_t d, uint32_t rows) {
+            bool add = false;
+#pragma unroll
+            for (int i = 0; i < kDK / 16; i++) {
+                const uint32_t at = rows + (i >> 2) * (kTileBytes / 2) + (i & 3) * 32;
+                tc::mma(tm + d, tm + kColS + 64 + 8 * i, tc::desc(at, 16, 1024), tc::idesc(kC, false), add);
+                add = true;
+                if (NP == 2) tc::mma(tm + d, tm + kColS + 8 * i, tc::desc(at + kTileBytes, 16, 1024), tc::idesc(kC, false), add);
+                tc::mma(tm + d, tm + kColS + 8 * i, tc::desc(at, 16, 1024), tc::idesc(kC, false), add);
+            }
+        };
+        // products of a [128][64] left operand with a lower-triangular square, transposed
+        auto with_square = [&](uint32_t d, uint32_t left, uint32_t square, int nk) {
+#pragma unroll
+            for (int i = 0; i < kC / 16; i++) {
+                if (i >= nk) break;
+                const uint32_t at = square + i * 2048 + i * 32, id = tc::idesc(kC - 16 * i, false);
+                tc::mma(tm + d + 16 * i, tm + left + 32 + 8 * i, tc::desc(at, 16, 1024), id, i > 0);
+                tc::mma(tm + d + 16 * i, tm + left + 8 * i, tc::desc(at + kSquareBytes / 2, 16, 1024), id, true);
+                tc::mma(tm + d + 16 * i, tm + left + 8 * i, tc::desc(at, 16, 1024), id, true);
+            }
+        };
+        // U' times the rows of K: the inner dimension runs over tokens
+        auto update = [&](uint32_t rows, int nk) {
+#pragma unroll
+            for (int i = 0; i < kC / 16; i++) {
+                if (i >= nk) break;
+                const uint32_t at = rows + i * 2048, id = tc::idesc(kDK, true);
+                tc::mma(tm + kColD, tm + kColY + 32 + 8 * i, tc::desc(at, kTileBytes / 2, 1024), id, i > 0);
+                if (NP == 2) tc::mma(tm + kColD, tm + kColY + 8 * i, tc::desc(at + kTileBytes, kTileBytes / 2, 1024), id, true);
+                tc::mma(tm + kColD, tm + kColY + 8 * i, tc::desc(at, kTileBytes / 2, 1024), id, true);
+            }
+        };
+        for (int it = 0; it < count; it++) {
+            const int par = it & 1, nk = (min(kC, row_end - row0 - it * kC) + 15) / 16;
+            const uint32_t kt = base + W::oK + it % W::kKStages * W::kKBytes;
+            const int kpar = (it / W::kKStages) & 1, qpar = (it >> 1) & 1;
+            // S is there: the block before has updated the state, and read its K and scales for the last time
+            wait(kGotS, par);
+            tc::fence_after();
             if (V != kLinear) {
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
-                        if (j >= 2 * nk) continue;
-                        uint32_t x[4];
-                        ldsm4(x, k0 + tile_at(8 * j + brow, 16 * i + bcol));
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            mma16816(y[j + e], lo[i][0], lo[i][1], lo[i][2], lo[i][3], x[2 * e], x[2 * e + 1]);
-                            mma16816(y[j + e], hi[i][0], hi[i][1], hi[i][2], hi[i][3], x[2 * e], x[2 * e + 1]);
-                        }
-                        if (NP == 2) {
-                            ldsm4(x, k0 + kTileBytes + tile_at(8 * j + brow, 16 * i + bcol));
-#pragma unroll
-                            for (int e = 0; e < 2; e++) mma16816(y[j + e], hi[i][0], hi[i][1], hi[i][2], hi[i][3], x[2 * e], x[2 * e + 1]);
-                        }
-                    }
-            }
-        }
-        if (V == kKda) release(kPartK, it);
-        if (!wait(&full[kPartInv], par)) return;
-        // r = beta (v - y)
-        {
-            const char *tile = vt + (it & 1) * kC * W::kVRow;
-            const uint32_t v0 = dev::smem_addr(tile);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                float v[2][4];  // of column tiles j, j + 1: rows g and g + 8, tokens 2 c, 2 c + 1
-                if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        v_pair(tile, 8 * (j + e) + 2 * c, g, &v[e][0], 0.f);
-                        v_pair(tile, 8 * (j + e) + 2 * c, g + 8, &v[e][2], 0.f);
-                    }
-                } else {
-                    // matrices: tokens 8 j.. x columns 0.., tokens 8 j.. x columns 8.., then tokens 8 (j + 1)..
-                    uint32_t x[4];
-                    ldsm4_t(x, v0 + (8 * j + (l & 7) + (l >> 4) * 8) * W::kVRow + ((l >> 3) & 1) * 16);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        float2 f;
-                        if constexpr (std::is_same<T, __half>::value)
-                            f = __half22float2(*reinterpret_cast<const __half2 *>(&x[e]));
-                        else
-                            f = make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u));
-                        v[e >> 1][2 * (e & 1)] = f.x;
-                        v[e >> 1][2 * (e & 1) + 1] = f.y;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int t = 8 * (j + e) + 2 * c;
-                    const float2 fy = *reinterpret_cast<const float2 *>(&sv[t]), be = *reinterpret_cast<const float2 *>(&sv[kC + t]);
-                    float *yy = y[j + e];
-                    yy[0] = be.x * fmaf(-yy[0], fy.x * sb0, v[e][0]);
-                    yy[1] = be.y * fmaf(-yy[1], fy.y * sb0, v[e][1]);
-                    yy[2] = be.x * fmaf(-yy[2], fy.x * sb1, v[e][2]);
-                    yy[3] = be.y * fmaf(-yy[3], fy.y * sb1, v[e][3]);
+                wait(kFullK + it % W::kKStages, kpar);
+                if (tc::elect()) {
+                    with_rows(kColY, kt);
+                    tc::commit(&bar[kDoneY]);
                 }
             }
-        }
-        uint32_t hi[4][4], lo[4][4];
-        float b0s, b1s;
-        if (V != kLinear) {
-            split_rows<8>(y, hi, lo, &b0s, &b1s);
-            // u = inv r: column tile j needs tokens s < 8 j + 8
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-#pragma unroll
-                for (int e = 0; e < 2; e++)
-#pragma unroll
-                    for (int d = 0; d < 4; d++) y[j + e][d] = 0.f;
-                if (j >= 2 * nk) continue;
-#pragma unroll
-                for (int i = 0; i <= j / 2; i++) {
-                    uint32_t x[4], z[4];
-                    ldsm4(x, inv0 + square_at(8 * j + brow, 16 * i + bcol));
-                    ldsm4(z, inv0 + kSquareBytes / 2 + square_at(8 * j + brow, 16 * i + bcol));
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        mma16816(y[j + e], lo[i][0], lo[i][1], lo[i][2], lo[i][3], x[2 * e], x[2 * e + 1]);
-                        mma16816(y[j + e], hi[i][0], hi[i][1], hi[i][2], hi[i][3], z[2 * e], z[2 * e + 1]);
-                        mma16816(y[j + e], hi[i][0], hi[i][1], hi[i][2], hi[i][3], x[2 * e], x[2 * e + 1]);
-                    }
+            if (it + 1 < count) {
+                if (V != kKda) copy_k(it + 1);
+                copy_sv(it + 1);
+            }
+            if (V == kKda && it > 0) copy(kFullK2, W::oK2, sc.k2 + tile(it), W::kKBytes);
+            if (V == kLinear) {  // the update does not wait for the state: it goes first
+                wait(kGotU, par);
+                tc::fence_after();
+                wait(kFullK + it % W::kKStages, kpar);
+                if (tc::elect()) {
+                    update(kt, nk);
+                    tc::commit(&bar[kDoneD]);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const float2 ft = *reinterpret_cast<const float2 *>(&sv[2 * kC + 8 * (j + e) + 2 * c]);
-                    y[j + e][0] *= ft.x * b0s; y[j + e][1] *= ft.y * b0s;
-                    y[j + e][2] *= ft.x * b1s; y[j + e][3] *= ft.y * b1s;
+            }
+            wait(kFullQ + (it & 1), qpar);
+            if (it > 0) wait(kReadSQ, par ^ 1);
+            tc::fence_after();
+            if (tc::elect()) {
+                with_rows(kColSQ, base + W::oQ + (it & 1) * W::kKBytes);
+                tc::commit(&bar[kDoneSQ]);
+            }
+            if (V != kLinear) {
+                wait(kGotR, par);
+                tc::fence_after();
+                wait(kFullInv, par);
+                if (tc::elect()) {
+                    with_square(kColU, kColY, base + W::oInv, nk);
+                    tc::commit(&bar[kDoneU]);
+                }
+                // Y is done, so U P^T of the block before is, too
+                if (V == kKda && it + 1 < count) copy_k(it + 1);
+                if (it > 0) copy(kFullP, W::oP, sc.p + bh(it) * kSquareBytes, kSquareBytes);
+                wait(kGotU, par);
+                tc::fence_after();
+                if (V == kKda) wait(kFullK2, par);
+                if (tc::elect()) {
+                    update(V == kKda ? base + W::oK2 : kt, nk);
+                    tc::commit(&bar[kDoneD]);
+                }
+                if (it + 1 < count) copy(kFullInv, W::oInv, sc.inv + bh(it + 1) * kSquareBytes, kSquareBytes);
+            }
+            wait(kFullP, par);
+            if (it > 0) wait(kReadUP, par ^ 1);
+            tc::fence_after();
+            if (tc::elect()) {
+                with_square(kColUP, kColU, base + W::oP, nk);
+                tc::commit(&bar[kDoneUP]);
+            }
+            if (it + 1 < count) {
+                copy_q(it + 1);
+                if (V == kLinear) {  // here nothing later tells that U P^T is done
+                    wait(kDoneUP, par);
+                    copy(kFullP, W::oP, sc.p + bh(it + 1) * kSquareBytes, kSquareBytes);
                 }
             }
         }
-        split_rows<8>(y, hi, lo, &b0s, &b1s);
-        if (!wait(uempty, par ^ 1)) return;
+        wait(kDoneUP, (count - 1) & 1);
+    } else if (w >= kStateWarps) {
+        // ---- output: a value column a thread ----
+        const int lane = 32 * (w & 3) + l;
+        const uint32_t tl = tm + ((uint32_t)(32 * (w & 3)) << 16);
+        T *out = static_cast<T *>(a.out) + (long long)h * kDV + lane;
+        const long long row = (long long)a.heads * kDV;
+        for (int it = 0; it < count; it++) {
+            const int par = it & 1, t0 = row0 + it * kC, n = min(kC, row_end - t0);
+            const float *ov = ov_all + (it & 1) * kOutFloats;
+            float2 o[kC / 2];
+            wait(kFullQ + (it & 1), (it >> 1) & 1);
+            wait(kDoneSQ, par);
+            tc::fence_after();
+            const float sb = s_back[(2 * (it & 1)) * kDV + lane];
+            tc::ld32(reinterpret_cast<uint32_t *>(o), tl + kColSQ);
+            tc::ld32(reinterpret_cast<uint32_t *>(o + 16), tl + kColSQ + 32);
+            tc::fence_before();
+            arrive(kReadSQ);
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            *reinterpret_cast<uint4 *>(xu + (2 * i) * 512 + l * 16) = make_uint4(hi[i][0], hi[i][1], hi[i][2], hi[i][3]);
-            *reinterpret_cast<uint4 *>(xu + (2 * i + 1) * 512 + l * 16) = make_uint4(lo[i][0], lo[i][1], lo[i][2], lo[i][3]);
-        }
-        if (c == 0) { xback[16 + g] = b0s; xback[24 + g] = b1s; }
-        __syncwarp();
-        if (l == 0) dev::mbar_arrive(ufull);
-        // u for the state: what of each token is left at the block's end
+            for (int t = 0; t < kC / 2; t++) o[t] = __fmul2_rn(o[t], __fmul2_rn(pair_at(ov + 2 * t), make_float2(sb, sb)));
+            wait(kDoneUP, par);
+            tc::fence_after();
+            const float ub = s_back[(2 * (it & 1) + 1) * kDV + lane];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float2 fu = *reinterpret_cast<const float2 *>(&sv[3 * kC + 8 * j + 2 * c]);
-            y[j][0] *= fu.x; y[j][1] *= fu.y; y[j][2] *= fu.x; y[j][3] *= fu.y;
-        }
-        split_rows<8>(y, hi, lo, &b0s, &b1s);
-        const float keep = V == kKda ? 0.f : sv[4 * kC];
-        if (V == kKda)
-            if (!wait(&full[kPartK2], par)) return;
-        if (V == kLinear && it > 0)
-            if (!wait(kfull, kpar)) return;
-        const uint32_t kk = V == kKda ? dev::smem_addr(smem + W::oK2) : k0;
+            for (int t1 = 0; t1 < kC / 2; t1 += 8) {
+                float2 p[8];
+                tc::ld16(reinterpret_cast<uint32_t *>(p), tl + kColUP + 2 * t1);
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            // sums start from zero and are added to the state once, rounded to nearest
-            float d[2][4] = {};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (i >= nk) continue;
-                uint32_t x[4];
-                // matrices: tokens 16 i.., 16 i + 8.. of key rows 8 j.., then of key rows 8 (j + 1)..
-                ldsm4_t(x, kk + tile_at(16 * i + (l & 15), 8 * j + (l >> 4) * 8));
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    mma16816(d[e], lo[i][0], lo[i][1], lo[i][2], lo[i][3], x[2 * e], x[2 * e + 1]);
-                    mma16816(d[e], hi[i][0], hi[i][1], hi[i][2], hi[i][3], x[2 * e], x[2 * e + 1]);
-                }
-                if (NP == 2) {
-                    ldsm4_t(x, kk + kTileBytes + tile_at(16 * i + (l & 15), 8 * j + (l >> 4) * 8));
-#pragma unroll
-                    for (int e = 0; e < 2; e++) mma16816(d[e], hi[i][0], hi[i][1], hi[i][2], hi[i][3], x[2 * e], x[2 * e + 1]);
-                }
+                for (int t = 0; t < 8; t++) o[t1 + t] = __ffma2_rn(p[t], __fmul2_rn(pair_at(ov + kC + 2 * (t1 + t)), make_float2(ub, ub)), o[t1 + t]);
             }
+            tc::fence_before();
+            arrive(kReadUP);
+            T *dst = out + (long long)t0 * row;
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                float2 kp = make_float2(keep, keep);
-                if (V == kKda) kp = *reinterpret_cast<const float2 *>(&sv[4 * kC + 8 * (j + e) + 2 * c]);
-                s[j + e][0] = fmaf(kp.x, s[j + e][0], d[e][0] * b0s);
-                s[j + e][1] = fmaf(kp.y, s[j + e][1], d[e][1] * b0s);
-                s[j + e][2] = fmaf(kp.x, s[j + e][2], d[e][2] * b1s);
-                s[j + e][3] = fmaf(kp.y, s[j + e][3], d[e][3] * b1s);
+            for (int t = 0; t < kC / 2; t++) {
+                if (2 * t < n) dst[0] = to_t<T>(o[t].x);
+                if (2 * t + 1 < n) dst[row] = to_t<T>(o[t].y);
+                dst += 2 * row;
             }
         }
-        release(kPartInv, it);
-        release(V == kKda ? kPartK2 : kPartK, it);
+    } else {
+        // ---- state: 64 key rows of a value column a thread ----
+        const int half = w >> 2, lane = 32 * (w & 3) + l;
+        const uint32_t tl = tm + ((uint32_t)(32 * (w & 3)) << 16);
+        float *Sp = a.S + ((long long)(a.by_slot ? live : r) * a.heads + h) * (kDK * kDV) + (64 * half) * kDV + lane;
+        float2 s[32];
+        const bool zero = a.p.fresh[r] != 0 && b0 == all0;
+#pragma unroll
+        for (int j = 0; j < 32; j++) s[j] = zero ? make_float2(0.f, 0.f) : make_float2(Sp[2 * j * kDV], Sp[(2 * j + 1) * kDV]);
+        const char *vt = smem + W::oV + 32 * half * W::kVRow;
+        auto v_pair = [&](int t) { return make_float2(v_at<T>(vt + 2 * t * W::kVRow, lane), v_at<T>(vt + (2 * t + 1) * W::kVRow, lane)); };
+        for (int it = 0; it < count; it++) {
+            const int par = it & 1;
+            // the block's scales: of this half's tokens
+            const float *sv = sv_all + (it & 1) * kStateFloats, *fy = sv + 32 * half, *be = fy + kC, *ft = be + kC, *fu = ft + kC;
+            float m[3], scale[3], back[3];
+            float2 y[16];
+            m[0] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; j++) m[0] = max_abs(m[0], s[j]);
+            if (V == kLinear) {
+                wait(kFullSv + (it & 1), (it >> 1) & 1);
+                wait(kFullV, par);
+                m[1] = m[2] = 0.f;
+#pragma unroll
+                for (int t = 0; t < 16; t++) {
+                    y[t] = __fmul2_rn(pair_at(be + 2 * t), v_pair(t));
+                    m[1] = max_abs(m[1], y[t]);
+                    m[2] = max_abs(m[2], __fmul2_rn(y[t], pair_at(fu + 2 * t)));
+                }
+                meet<3>(s_max, half, lane, m, scale, back);
+                // the products of the block before have read the halves of U
+                if (it > 0) wait(kDoneUP, par ^ 1);
+                tc::fence_after();
+                store_halves<16>(tl + kColY + 16 * half, tl + kColY + 32 + 16 * half, scale[2], [&](int t) { return __fmul2_rn(y[t], pair_at(fu + 2 * t)); });
+                store_halves<16>(tl + kColU + 16 * half, tl + kColU + 32 + 16 * half, scale[1], [&](int t) { return y[t]; });
+                store_halves<32>(tl + kColS + 32 * half, tl + kColS + 64 + 32 * half, scale[0], [&](int j) { return s[j]; });
+                if (half == 0) {
+                    s_back[(2 * (it & 1)) * kDV + lane] = back[0];
+                    s_back[(2 * (it & 1) + 1) * kDV + lane] = back[1];
+                }
+                back[1] = back[2];
+                tc::wait_st();
+                tc::fence_before();
+                arrive(kGotS);
+                arrive(kGotU);
+            } else {
+                meet<1>(s_max, half, lane, m, scale, back);
+                const float sb = back[0];
+                store_halves<32>(tl + kColS + 32 * half, tl + kColS + 64 + 32 * half, scale[0], [&](int j) { return s[j]; });
+                if (half == 0) s_back[(2 * (it & 1)) * kDV + lane] = sb;
+                tc::wait_st();
+                tc::fence_before();
+                arrive(kGotS);
+                // r = beta (v - y)
+                wait(kFullSv + (it & 1), (it >> 1) & 1);
+                wait(kFullV, par);
+                wait(kDoneY, par);
+                tc::fence_after();
+                tc::ld32(reinterpret_cast<uint32_t *>(y), tl + kColY + 32 * half);
+                m[0] = 0.f;
+#pragma unroll
+                for (int t = 0; t < 16; t++) {
+                    const float2 f = __fmul2_rn(pair_at(fy + 2 * t), make_float2(-sb, -sb));
+                    y[t] = __fmul2_rn(pair_at(be + 2 * t), __ffma2_rn(y[t], f, v_pair(t)));
+                    m[0] = max_abs(m[0], y[t]);
+                }
+                meet<1>(s_max + 2 * kDV, half, lane, m, scale, back);
+                store_halves<16>(tl + kColY + 16 * half, tl + kColY + 32 + 16 * half, scale[0], [&](int t) { return y[t]; });
+                tc::wait_st();
+                tc::fence_before();
+                arrive(kGotR);
+                // u = inv r, and what of it is left at the block's end
+                wait(kDoneU, par);
+                tc::fence_after();
+                const float2 rb = make_float2(back[0], back[0]);
+                tc::ld32(reinterpret_cast<uint32_t *>(y), tl + kColU + 32 * half);
+                m[0] = m[1] = 0.f;
+#pragma unroll
+                for (int t = 0; t < 16; t++) {
+                    y[t] = __fmul2_rn(y[t], __fmul2_rn(pair_at(ft + 2 * t), rb));
+                    m[0] = max_abs(m[0], y[t]);
+                    m[1] = max_abs(m[1], __fmul2_rn(y[t], pair_at(fu + 2 * t)));
+                }
+                meet<2>(s_max, half, lane, m, scale, back);
+                store_halves<16>(tl + kColY + 16 * half, tl + kColY + 32 + 16 * half, scale[1], [&](int t) { return __fmul2_rn(y[t], pair_at(fu + 2 * t)); });
+                store_halves<16>(tl + kColU + 16 * half, tl + kColU + 32 + 16 * half, scale[0], [&](int t) { return y[t]; });
+                if (half == 0) s_back[(2 * (it & 1) + 1) * kDV + lane] = back[0];
+                tc::wait_st();
+                tc::fence_before();
+                arrive(kGotU);
+            }
+            wait(kDoneD, par);
+            tc::fence_after();
+            const float2 ub = make_float2(back[1], back[1]);
+            const float keep = V == kKda ? 0.f : sv[4 * kC];
+#pragma unroll
+            for (int j1 = 0; j1 < 32; j1 += 8) {
+                float2 d[8];
+                tc::ld16(reinterpret_cast<uint32_t *>(d), tl + kColD + 64 * half + 2 * j1);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const float2 kp = V == kKda ? pair_at(sv + 4 * kC + 64 * half + 2 * (j1 + j)) : make_float2(keep, keep);
+                    s[j1 + j] = __ffma2_rn(kp, s[j1 + j], __fmul2_rn(d[j], ub));
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j++) {
+            Sp[2 * j * kDV] = s[j].x;
+            Sp[(2 * j + 1) * kDV] = s[j].y;
+        }
     }
-#pragma unroll
-    for (int j = 0; j < 16; j++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) Sp[(8 * j + 2 * c + (e & 1)) * kDV + 8 * (e >> 1)] = s[j][e];
+    tc::fence_before();
+    __syncthreads();
+    if (w == kIssueWarp) tc::dealloc(tm, kColumns);
 }
 
 // Blocks of a launch: the scratch stays near this size however long the batch is.
@@ -857,14 +856,13 @@ cudaError_t launch_tiles(const PromptArgs &a, int first, int n, const Scratch &s
     return cudaGetLastError();
 }
 
-template <class T, int V, int NP, int NR>
+template <class T, int V, int NP>
 cudaError_t launch_walk(const PromptArgs &a, int first, int n, const Scratch &sc, cudaStream_t s)
 {
-    using W = Walk<T, V, NP, NR>;
-    cudaError_t e = cudaFuncSetAttribute(k_block_walk<T, V, NP, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes);
+    using W = Walk<T, V, NP>;
+    cudaError_t e = cudaFuncSetAttribute(k_block_walk<T, V, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, W::kBytes);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)a.p.requests * (unsigned)a.heads * (kDV / (16 * NR));
-    k_block_walk<T, V, NP, NR><<<grid, W::kThreads, W::kBytes, s>>>(a, first, n, sc);
+    k_block_walk<T, V, NP><<<(unsigned)a.p.requests * (unsigned)a.heads, kWalkThreads, W::kBytes, s>>>(a, first, n, sc);
     return cudaGetLastError();
 }
 
@@ -873,12 +871,11 @@ cudaError_t launch_t(const PromptArgs &a, cudaStream_t s)
 {
     const int step = launch_blocks(a);
     const Scratch sc = scratch_of(a.variant, a.dtype, a.heads, a.share, step);
-    const long long items = (long long)a.p.requests * a.heads;
     for (int first = 0; first < a.p.blocks; first += step) {
         const int n = std::min(step, a.p.blocks - first);
         cudaError_t e = launch_tiles<T, V, NP>(a, first, n, sc, s);
         if (e != cudaSuccess) return e;
-        e = items >= 74 ? launch_walk<T, V, NP, 4>(a, first, n, sc, s) : launch_walk<T, V, NP, 2>(a, first, n, sc, s);
+        e = launch_walk<T, V, NP>(a, first, n, sc, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
