@@ -5,10 +5,12 @@
 //   A_ts = beta_t sum_d k_td decay_ts,d k_sd (s < t),     P_ts = sum_d q_td decay_ts,d k_sd (s <= t),
 //   U = (I + A)^-1 (beta (V - (c K) S)),
 //   out = (c Q) S + P U,        S <- c_64 S + (decay_64 K)^T U
-// (plain linear attention: U = beta V).  What does not depend on the state --
-// (I + A)^-1, P and the operands in the form the tensor cores take -- is made
-// for all blocks at once by a first kernel; a second walks each request's
-// blocks in order and carries the state in registers.
+// (plain linear attention: U = beta V).  What does not depend on the state is
+// made for all blocks at once by a first kernel: decay_64 (I + A)^-1, which
+// takes the residual R = beta (V - (c K) S) to the U the state's update needs,
+// P (I + A)^-1, which takes it to the output, and the operands in the form the
+// tensor cores take.  A second kernel walks each request's blocks in order and
+// carries the state in registers.
 //
 // Every product runs on the tensor cores with its fp32 operands split into two
 // binary16 halves (three products, two where an operand is exact in binary16),
@@ -36,9 +38,10 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kC = kBlockTokens;
 constexpr int kTileBytes = kC * kDK * 2;    // one binary16 half of a [64][128] operand
 constexpr int kSquareBytes = kC * kC * 2 * 2;  // hi and lo of a [64][64] operand
-// per block and head, for the state: unscale of the K rows times c_t, beta,
-// unscale of the inverse's rows, scale of U for the state update, kept share of S
-constexpr int kStateFloats = 4 * kC + kDK;
+// per block and head, for the state: -beta c_t times the unscale of the K rows, beta,
+// unscale of the rows that make U (plain linear attention: what of each token
+// is left at the block's end, times the unscale of its K row), kept share of S
+constexpr int kStateFloats = 3 * kC + kDK;
 constexpr int kOutFloats = 2 * kC;          // for the output: unscale of the Q rows times c_t, of the P rows
 constexpr long long kWaitLimit = 1LL << 32;  // cycles, about two seconds
 
@@ -245,6 +248,38 @@ __device__ void invert_lower(const float *A, float *inv, float *tmp)
     }
 }
 
+// out = X Y for lower-triangular X and Y [64][64] (shared memory, 256 threads;
+// a thread makes 4 x 4 outputs).  The blocks of 16 x 16 on and below the
+// diagonal are written.
+__device__ void lower_product(const float *X, const float *Y, float *out)
+{
+    const int i0 = 4 * (threadIdx.x >> 4), j0 = 4 * (threadIdx.x & 15);
+    if ((j0 & ~15) > i0) return;
+    float acc[4][4] = {};
+    // both are zero above their diagonals: inner indices from the columns' block to the rows'
+    for (int m = j0 & ~3; m < i0 + 4; m += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            x[e] = *reinterpret_cast<const float4 *>(X + (i0 + e) * kLd + m);
+            y[e] = *reinterpret_cast<const float4 *>(Y + (m + e) * kLd + j0);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const float xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+            for (int d = 0; d < 4; d++) {
+                acc[e][0] = fmaf(xs[d], y[d].x, acc[e][0]);
+                acc[e][1] = fmaf(xs[d], y[d].y, acc[e][1]);
+                acc[e][2] = fmaf(xs[d], y[d].z, acc[e][2]);
+                acc[e][3] = fmaf(xs[d], y[d].w, acc[e][3]);
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++) *reinterpret_cast<float4 *>(out + (i0 + e) * kLd + j0) = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
+}
+
 // What a tile kernel's CTA works on: a block of a live request.
 struct Block {
     int b, r, t0, n;  // block of this launch, request, first token row, tokens
@@ -271,7 +306,7 @@ template <class T, int V, int NP>
 __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_block, Scratch sc)
 {
     extern __shared__ __align__(1024) char smem[];
-    __shared__ float ek[kC], eq[kC], s_alpha[kC], s_beta[kC], s_inv[kC], s_p[kC];
+    __shared__ float ek[kC], eq[kC], s_alpha[kC], s_beta[kC], s_left[kC], s_inv[kC], s_p[kC];
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
     const int heads_k = a.heads / a.share;
     Block k;
@@ -359,19 +394,26 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
         const float a0 = s_alpha[0];
         if (tid < kC) {
             const float ct = sD[tid * kLd] * a0;
-            sv[tid] = ct * ek[tid];
+            sv[tid] = -s_beta[tid] * ct * ek[tid];
             sv[kC + tid] = s_beta[tid];
-            sv[3 * kC + tid] = sD[(kC - 1) * kLd + tid] * ek[tid];
+            // what of the token is left at the block's end, times the unscale of its K row in the update
+            s_left[tid] = sD[(kC - 1) * kLd + tid] * ek[tid];
             ov[tid] = ct * eq[tid];
-            if (tid == 0) sv[4 * kC] = sD[(kC - 1) * kLd] * a0;
+            if (tid == 0) sv[3 * kC] = sD[(kC - 1) * kLd] * a0;
         }
         __syncthreads();
-        if (V != kLinear) invert_lower(sA, sI, sD);
-        put_square(sP, reinterpret_cast<char *>(a.scratch) + sc.p + bh * kSquareBytes, s_p);
+        float *out = sP;
+        if (V != kLinear) {
+            invert_lower(sA, sI, sD);
+            lower_product(sP, sI, sA);
+            __syncthreads();
+            out = sA;
+        }
+        put_square(out, reinterpret_cast<char *>(a.scratch) + sc.p + bh * kSquareBytes, s_p);
         if (V != kLinear) put_square(sI, reinterpret_cast<char *>(a.scratch) + sc.inv + bh * kSquareBytes, s_inv);
         __syncthreads();
         if (tid < kC) {
-            sv[2 * kC + tid] = V == kLinear ? 1.f : s_inv[tid];
+            sv[2 * kC + tid] = V == kLinear ? s_left[tid] : s_inv[tid] * s_left[tid];
             ov[kC + tid] = s_p[tid];
         }
     }
@@ -383,18 +425,19 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
 // as the 128 lanes of tensor memory, so that each product's result, read from
 // tensor memory by the threads of its lanes, scaled and split, goes back there
 // as the next product's left operand:
-//   Y = S^T K^T  ->  R = beta (V^T - Y)  ->  U = R inv^T  ->  S^T <- keep S^T + U' K,
-//   out^T = S^T Q^T + U P^T.
-// Warps 0-7 keep the state (64 key rows of one value column a thread) and walk
-// this chain; warps 8-11 finish the output, off the chain; warp 12 issues the
-// products and the copies of the operands, warp 13 copies V.  Sums in tensor memory never pass
-// from block to block: the state is updated in registers, rounded to nearest.
+//   Y = S^T K^T  ->  R = beta (V^T - Y)  ->  U = R (decay inv)^T  ->  S^T <- keep S^T + U K,
+//   out^T = S^T Q^T + R (P inv)^T.
+// Warps 0-15 keep the state (32 key rows of one value column a thread) and walk
+// this chain; warps 16-19 finish the output, off the chain; warp 20 issues the
+// products and the copies of the operands, warp 21 copies V.  Sums in tensor
+// memory never pass from block to block: the state is updated in registers,
+// rounded to nearest.
 // ---------------------------------------------------------------------------
-constexpr int kStateWarps = 8, kOutWarps = 4;
+constexpr int kStateWarps = 16, kOutWarps = 4;
 constexpr int kIssueWarp = kStateWarps + kOutWarps, kValueWarp = kIssueWarp + 1;
 constexpr int kWalkThreads = 32 * (kValueWarp + 1);
-// columns of tensor memory: Y, then the halves of R, then of U'; S^T Q^T; U,
-// then its halves; U P^T; the state's update; the halves of S
+// columns of tensor memory: Y, then the halves of R; S^T Q^T; U, then its
+// halves; the output's second part; the state's update; the halves of S
 constexpr int kColY = 0, kColSQ = 64, kColU = 128, kColUP = 192, kColD = 256, kColS = 384, kColumns = 512;
 
 template <class T, int V, int NP>
@@ -413,8 +456,8 @@ struct Walk {
     static constexpr int oV = oP + kSquareBytes;
     static constexpr int oSv = oV + kC * kVRow;
     static constexpr int oOv = oSv + 2 * kStateFloats * 4;
-    static constexpr int oMax = oOv + 2 * kOutFloats * 4;   // [3][2][128] row maxima of the two halves of the state warps
-    static constexpr int oBack = oMax + 3 * 2 * kDV * 4;    // [2][2][128] unscales of S and U
+    static constexpr int oMax = oOv + 2 * kOutFloats * 4;   // [3][4][128] row maxima of the four quarters of the state warps
+    static constexpr int oBack = oMax + 3 * 4 * kDV * 4;    // [2][2][128] unscales of S and R
     static constexpr int oBar = oBack + 2 * 2 * kDV * 4;
     static constexpr int oFlags = oBar + 8 * 32;            // tensor memory address; whether a wait gave up
     static constexpr int kBytes = oFlags + 8;
@@ -423,24 +466,31 @@ struct Walk {
 
 // Barriers.  Copies: K (2), Q with the output's scales (2), K2, the inverse, P,
 // V, the state's scales (2).  Products done: Y, S^T Q^T, U, U P^T, update.
-// Halves written: S, R, U.  Output read: S^T Q^T, U P^T.
-enum { kFullK = 0, kFullQ = 2, kFullK2 = 4, kFullInv, kFullP, kFullV, kFullSv, kDoneY = 10, kDoneSQ, kDoneU, kDoneUP, kDoneD, kGotS, kGotR, kGotU, kReadSQ, kReadUP, kBarriers };
+// Halves written: the even 16 key rows of S, and the odd ones; R, U.  Output
+// read: S^T Q^T, U P^T.  The update's product comes in two, 64 key rows each.
+enum {
+    kFullK = 0, kFullQ = 2, kFullK2 = 4, kFullInv, kFullP, kFullV, kFullSv, kDoneY = 10, kDoneSQ, kDoneU, kDoneUP, kDoneD,
+    kGotS0 = kDoneD + 2, kGotS, kGotR, kGotU, kReadSQ, kReadUP, kBarriers
+};
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dev::smem_addr(dst)), "l"(src) : "memory");
 }
 
-// Row maxima of the two halves of the state warps, exchanged: scale and unscale
-// of N rows (one a thread), in one meeting of the 256 threads.
+// Row maxima of the four quarters of the state warps, exchanged: scale and
+// unscale of N rows (one a thread), in one meeting of the 512 threads.
 template <int N>
-__device__ __forceinline__ void meet(float *sm, int half, int lane, const float *m, float *scale, float *back)
+__device__ __forceinline__ void meet(float *sm, int quarter, int lane, const float *m, float *scale, float *back)
 {
 #pragma unroll
-    for (int i = 0; i < N; i++) sm[(2 * i + half) * kDV + lane] = m[i];
-    asm volatile("bar.sync 1, 256;" ::: "memory");
+    for (int i = 0; i < N; i++) sm[(4 * i + quarter) * kDV + lane] = m[i];
+    asm volatile("bar.sync 1, 512;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < N; i++) dev::row_scale(fmaxf(m[i], sm[(2 * i + (half ^ 1)) * kDV + lane]), &scale[i], &back[i]);
+    for (int i = 0; i < N; i++) {
+        const float *x = sm + 4 * i * kDV + lane;
+        dev::row_scale(fmaxf(fmaxf(x[0], x[kDV]), fmaxf(x[2 * kDV], x[3 * kDV])), &scale[i], &back[i]);
+    }
 }
 
 // N pairs x(i) of a row's numbers, times its scale, as halves into tensor memory.
@@ -459,7 +509,12 @@ __device__ __forceinline__ void store_halves(uint32_t hi_at, uint32_t lo_at, flo
 }
 
 // The larger of m and the magnitudes of a pair.
-__device__ __forceinline__ float max_abs(float m, float2 x) { return fmaxf(fmaxf(m, fabsf(x.x)), fabsf(x.y)); }
+__device__ __forceinline__ float max_abs(float m, float2 x)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(x.x)), "f"(fabsf(x.y)));
+    return r;
+}
 
 __device__ __forceinline__ float2 pair_at(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
@@ -503,7 +558,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
         *s_dead = (dev::smem_addr(smem) & 1023) != 0;
         if (*s_dead) atomicOr(a.p.head, kPlanTimeout);
         for (int i = 0; i < kBarriers; i++)
-            dev::mbar_init(&bar[i], i == kGotS || i == kGotR || i == kGotU ? kStateWarps : (i == kReadSQ || i == kReadUP ? kOutWarps : (i == kFullV ? 32 : 1)));
+            dev::mbar_init(&bar[i], i == kGotS0 || i == kGotS || i == kGotR || i == kGotU ? kStateWarps : (i == kReadSQ || i == kReadUP ? kOutWarps : (i == kFullV ? 32 : 1)));
         dev::fence_barrier_init();
     }
     // rows of V behind the request's last are multiplied by zero: they must be finite
@@ -574,10 +629,10 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
         copy(kFullP, W::oP, sc.p + bh(0) * kSquareBytes, kSquareBytes);
         const uint32_t base = dev::smem_addr(smem);
         // products of S^T with the rows of an operand tile
-        auto with_rows = [&](uint32_t d, uint32_t rows) {
-            bool add = false;
+        auto with_rows = [&](uint32_t d, uint32_t rows, int odd) {
+            bool add = odd != 0;
 #pragma unroll
-            for (int i = 0; i < kDK / 16; i++) {
+            for (int i = odd; i < kDK / 16; i += 2) {
                 const uint32_t at = rows + (i >> 2) * (kTileBytes / 2) + (i & 3) * 32;
                 tc::mma(tm + d, tm + kColS + 64 + 8 * i, tc::desc(at, 16, 1024), tc::idesc(kC, false), add);
                 add = true;
@@ -596,50 +651,59 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
                 tc::mma(tm + d + 16 * i, tm + left + 8 * i, tc::desc(at, 16, 1024), id, true);
             }
         };
-        // U' times the rows of K: the inner dimension runs over tokens
+        // U times 64 columns of the rows of K: the inner dimension runs over tokens
         auto update = [&](uint32_t rows, int nk) {
 #pragma unroll
-            for (int i = 0; i < kC / 16; i++) {
-                if (i >= nk) break;
-                const uint32_t at = rows + i * 2048, id = tc::idesc(kDK, true);
-                tc::mma(tm + kColD, tm + kColY + 32 + 8 * i, tc::desc(at, kTileBytes / 2, 1024), id, i > 0);
-                if (NP == 2) tc::mma(tm + kColD, tm + kColY + 8 * i, tc::desc(at + kTileBytes, kTileBytes / 2, 1024), id, true);
-                tc::mma(tm + kColD, tm + kColY + 8 * i, tc::desc(at, kTileBytes / 2, 1024), id, true);
+            for (int e = 0; e < 2; e++) {
+#pragma unroll
+                for (int i = 0; i < kC / 16; i++) {
+                    if (i >= nk) break;
+                    const uint32_t at = rows + e * (kTileBytes / 2) + i * 2048, id = tc::idesc(kDK / 2, true), d = tm + kColD + 64 * e;
+                    tc::mma(d, tm + kColU + 32 + 8 * i, tc::desc(at, kTileBytes / 2, 1024), id, i > 0);
+                    if (NP == 2) tc::mma(d, tm + kColU + 8 * i, tc::desc(at + kTileBytes, kTileBytes / 2, 1024), id, true);
+                    tc::mma(d, tm + kColU + 8 * i, tc::desc(at, kTileBytes / 2, 1024), id, true);
+                }
+                tc::commit(&bar[kDoneD + e]);
             }
         };
         for (int it = 0; it < count; it++) {
             const int par = it & 1, nk = (min(kC, row_end - row0 - it * kC) + 15) / 16;
             const uint32_t kt = base + W::oK + it % W::kKStages * W::kKBytes;
             const int kpar = (it / W::kKStages) & 1, qpar = (it >> 1) & 1;
-            // S is there: the block before has updated the state, and read its K and scales for the last time
-            wait(kGotS, par);
+            // S is there: the block before has updated the state, and read its
+            // K, its P and its scales for the last time
+            wait(kGotS0, par);
             tc::fence_after();
             if (V != kLinear) {
                 wait(kFullK + it % W::kKStages, kpar);
-                if (tc::elect()) {
-                    with_rows(kColY, kt);
-                    tc::commit(&bar[kDoneY]);
-                }
+                if (tc::elect()) with_rows(kColY, kt, 0);
+            }
+            wait(kGotS, par);
+            tc::fence_after();
+            if (V != kLinear && tc::elect()) {
+                with_rows(kColY, kt, 1);
+                tc::commit(&bar[kDoneY]);
             }
             if (it + 1 < count) {
                 if (V != kKda) copy_k(it + 1);
                 copy_sv(it + 1);
             }
-            if (V == kKda && it > 0) copy(kFullK2, W::oK2, sc.k2 + tile(it), W::kKBytes);
-            if (V == kLinear) {  // the update does not wait for the state: it goes first
+            if (it > 0) {
+                copy(kFullP, W::oP, sc.p + bh(it) * kSquareBytes, kSquareBytes);
+                if (V == kKda) copy(kFullK2, W::oK2, sc.k2 + tile(it), W::kKBytes);
+            }
+            if (V == kLinear) {
                 wait(kGotU, par);
                 tc::fence_after();
                 wait(kFullK + it % W::kKStages, kpar);
-                if (tc::elect()) {
-                    update(kt, nk);
-                    tc::commit(&bar[kDoneD]);
-                }
+                if (tc::elect()) update(kt, nk);
             }
             wait(kFullQ + (it & 1), qpar);
             if (it > 0) wait(kReadSQ, par ^ 1);
             tc::fence_after();
             if (tc::elect()) {
-                with_rows(kColSQ, base + W::oQ + (it & 1) * W::kKBytes);
+                with_rows(kColSQ, base + W::oQ + (it & 1) * W::kKBytes, 0);
+                with_rows(kColSQ, base + W::oQ + (it & 1) * W::kKBytes, 1);
                 tc::commit(&bar[kDoneSQ]);
             }
             if (V != kLinear) {
@@ -650,31 +714,22 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
                     with_square(kColU, kColY, base + W::oInv, nk);
                     tc::commit(&bar[kDoneU]);
                 }
-                // Y is done, so U P^T of the block before is, too
                 if (V == kKda && it + 1 < count) copy_k(it + 1);
-                if (it > 0) copy(kFullP, W::oP, sc.p + bh(it) * kSquareBytes, kSquareBytes);
-                wait(kGotU, par);
-                tc::fence_after();
-                if (V == kKda) wait(kFullK2, par);
-                if (tc::elect()) {
-                    update(V == kKda ? base + W::oK2 : kt, nk);
-                    tc::commit(&bar[kDoneD]);
-                }
-                if (it + 1 < count) copy(kFullInv, W::oInv, sc.inv + bh(it + 1) * kSquareBytes, kSquareBytes);
             }
             wait(kFullP, par);
             if (it > 0) wait(kReadUP, par ^ 1);
             tc::fence_after();
             if (tc::elect()) {
-                with_square(kColUP, kColU, base + W::oP, nk);
+                with_square(kColUP, kColY, base + W::oP, nk);
                 tc::commit(&bar[kDoneUP]);
             }
-            if (it + 1 < count) {
-                copy_q(it + 1);
-                if (V == kLinear) {  // here nothing later tells that U P^T is done
-                    wait(kDoneUP, par);
-                    copy(kFullP, W::oP, sc.p + bh(it + 1) * kSquareBytes, kSquareBytes);
-                }
+            if (it + 1 < count) copy_q(it + 1);  // the output of the block before is out
+            if (V != kLinear) {
+                wait(kGotU, par);
+                tc::fence_after();
+                if (V == kKda) wait(kFullK2, par);
+                if (tc::elect()) update(V == kKda ? base + W::oK2 : kt, nk);
+                if (it + 1 < count) copy(kFullInv, W::oInv, sc.inv + bh(it + 1) * kSquareBytes, kSquareBytes);
             }
         }
         wait(kDoneUP, (count - 1) & 1);
@@ -687,146 +742,146 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
         for (int it = 0; it < count; it++) {
             const int par = it & 1, t0 = row0 + it * kC, n = min(kC, row_end - t0);
             const float *ov = ov_all + (it & 1) * kOutFloats;
-            float2 o[kC / 2];
             wait(kFullQ + (it & 1), (it >> 1) & 1);
             wait(kDoneSQ, par);
-            tc::fence_after();
-            const float sb = s_back[(2 * (it & 1)) * kDV + lane];
-            tc::ld32(reinterpret_cast<uint32_t *>(o), tl + kColSQ);
-            tc::ld32(reinterpret_cast<uint32_t *>(o + 16), tl + kColSQ + 32);
-            tc::fence_before();
-            arrive(kReadSQ);
-#pragma unroll
-            for (int t = 0; t < kC / 2; t++) o[t] = __fmul2_rn(o[t], __fmul2_rn(pair_at(ov + 2 * t), make_float2(sb, sb)));
             wait(kDoneUP, par);
             tc::fence_after();
-            const float ub = s_back[(2 * (it & 1) + 1) * kDV + lane];
-#pragma unroll
-            for (int t1 = 0; t1 < kC / 2; t1 += 8) {
-                float2 p[8];
-                tc::ld16(reinterpret_cast<uint32_t *>(p), tl + kColUP + 2 * t1);
-#pragma unroll
-                for (int t = 0; t < 8; t++) o[t1 + t] = __ffma2_rn(p[t], __fmul2_rn(pair_at(ov + kC + 2 * (t1 + t)), make_float2(ub, ub)), o[t1 + t]);
-            }
-            tc::fence_before();
-            arrive(kReadUP);
+            const float sb = s_back[(2 * (it & 1)) * kDV + lane], rb = s_back[(2 * (it & 1) + 1) * kDV + lane];
             T *dst = out + (long long)t0 * row;
 #pragma unroll
-            for (int t = 0; t < kC / 2; t++) {
-                if (2 * t < n) dst[0] = to_t<T>(o[t].x);
-                if (2 * t + 1 < n) dst[row] = to_t<T>(o[t].y);
-                dst += 2 * row;
+            for (int t1 = 0; t1 < kC; t1 += 16) {
+                float2 o[8], p[8];
+                tc::ld16(reinterpret_cast<uint32_t *>(o), tl + kColSQ + t1);
+                tc::ld16(reinterpret_cast<uint32_t *>(p), tl + kColUP + t1);
+#pragma unroll
+                for (int t = 0; t < 8; t++) {
+                    const float2 fq = __fmul2_rn(pair_at(ov + t1 + 2 * t), make_float2(sb, sb)), fp = __fmul2_rn(pair_at(ov + kC + t1 + 2 * t), make_float2(rb, rb));
+                    o[t] = __ffma2_rn(p[t], fp, __fmul2_rn(o[t], fq));
+                    if (t1 + 2 * t < n) dst[0] = to_t<T>(o[t].x);
+                    if (t1 + 2 * t + 1 < n) dst[row] = to_t<T>(o[t].y);
+                    dst += 2 * row;
+                }
             }
+            tc::fence_before();
+            arrive(kReadSQ);
+            arrive(kReadUP);
         }
     } else {
-        // ---- state: 64 key rows of a value column a thread ----
-        const int half = w >> 2, lane = 32 * (w & 3) + l;
+        // ---- state: 32 key rows of a value column a thread ----
+        const int part = w >> 2, lane = 32 * (w & 3) + l;  // quarter of the key rows, and of the tokens; value column
         const uint32_t tl = tm + ((uint32_t)(32 * (w & 3)) << 16);
-        float *Sp = a.S + ((long long)(a.by_slot ? live : r) * a.heads + h) * (kDK * kDV) + (64 * half) * kDV + lane;
-        float2 s[32];
+        float *Sp = a.S + ((long long)(a.by_slot ? live : r) * a.heads + h) * (kDK * kDV) + (32 * part) * kDV + lane;
+        float2 s[16];
         const bool zero = a.p.fresh[r] != 0 && b0 == all0;
 #pragma unroll
-        for (int j = 0; j < 32; j++) s[j] = zero ? make_float2(0.f, 0.f) : make_float2(Sp[2 * j * kDV], Sp[(2 * j + 1) * kDV]);
-        const char *vt = smem + W::oV + 32 * half * W::kVRow;
+        for (int j = 0; j < 16; j++) s[j] = zero ? make_float2(0.f, 0.f) : make_float2(Sp[2 * j * kDV], Sp[(2 * j + 1) * kDV]);
+        const char *vt = smem + W::oV + 16 * part * W::kVRow;
         auto v_pair = [&](int t) { return make_float2(v_at<T>(vt + 2 * t * W::kVRow, lane), v_at<T>(vt + (2 * t + 1) * W::kVRow, lane)); };
+        // 16 key rows of the 32, and word of them
+        auto store_s = [&](int e, float scale) {
+            const uint32_t at = tl + kColS + 16 * part + 8 * e;
+            store_halves<8>(at, at + 64, scale, [&](int j) { return s[8 * e + j]; });
+            tc::wait_st();
+            tc::fence_before();
+            arrive(e == 0 ? kGotS0 : kGotS);
+        };
         for (int it = 0; it < count; it++) {
             const int par = it & 1;
-            // the block's scales: of this half's tokens
-            const float *sv = sv_all + (it & 1) * kStateFloats, *fy = sv + 32 * half, *be = fy + kC, *ft = be + kC, *fu = ft + kC;
+            // the block's scales: of this quarter's tokens
+            const float *sv = sv_all + (it & 1) * kStateFloats, *fy = sv + 16 * part, *be = fy + kC, *fu = be + kC;
+            float *s_out = s_back + (2 * (it & 1)) * kDV + lane;  // unscales of S and R for the output
             float m[3], scale[3], back[3];
-            float2 y[16];
+            float2 y[8];
             m[0] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 32; j++) m[0] = max_abs(m[0], s[j]);
+            for (int j = 0; j < 16; j++) m[0] = max_abs(m[0], s[j]);
             if (V == kLinear) {
                 wait(kFullSv + (it & 1), (it >> 1) & 1);
                 wait(kFullV, par);
                 m[1] = m[2] = 0.f;
 #pragma unroll
-                for (int t = 0; t < 16; t++) {
+                for (int t = 0; t < 8; t++) {
                     y[t] = __fmul2_rn(pair_at(be + 2 * t), v_pair(t));
                     m[1] = max_abs(m[1], y[t]);
                     m[2] = max_abs(m[2], __fmul2_rn(y[t], pair_at(fu + 2 * t)));
                 }
-                meet<3>(s_max, half, lane, m, scale, back);
-                // the products of the block before have read the halves of U
+                meet<3>(s_max, part, lane, m, scale, back);
+                // the output of the block before has read the halves of R
                 if (it > 0) wait(kDoneUP, par ^ 1);
                 tc::fence_after();
-                store_halves<16>(tl + kColY + 16 * half, tl + kColY + 32 + 16 * half, scale[2], [&](int t) { return __fmul2_rn(y[t], pair_at(fu + 2 * t)); });
-                store_halves<16>(tl + kColU + 16 * half, tl + kColU + 32 + 16 * half, scale[1], [&](int t) { return y[t]; });
-                store_halves<32>(tl + kColS + 32 * half, tl + kColS + 64 + 32 * half, scale[0], [&](int j) { return s[j]; });
-                if (half == 0) {
-                    s_back[(2 * (it & 1)) * kDV + lane] = back[0];
-                    s_back[(2 * (it & 1) + 1) * kDV + lane] = back[1];
+                store_halves<8>(tl + kColU + 8 * part, tl + kColU + 32 + 8 * part, scale[2], [&](int t) { return __fmul2_rn(y[t], pair_at(fu + 2 * t)); });
+                store_halves<8>(tl + kColY + 8 * part, tl + kColY + 32 + 8 * part, scale[1], [&](int t) { return y[t]; });
+                if (part == 0) {
+                    s_out[0] = back[0];
+                    s_out[kDV] = back[1];
                 }
-                back[1] = back[2];
                 tc::wait_st();
                 tc::fence_before();
-                arrive(kGotS);
                 arrive(kGotU);
+                store_s(0, scale[0]);
+                store_s(1, scale[0]);
             } else {
-                meet<1>(s_max, half, lane, m, scale, back);
-                const float sb = back[0];
-                store_halves<32>(tl + kColS + 32 * half, tl + kColS + 64 + 32 * half, scale[0], [&](int j) { return s[j]; });
-                if (half == 0) s_back[(2 * (it & 1)) * kDV + lane] = sb;
-                tc::wait_st();
-                tc::fence_before();
-                arrive(kGotS);
-                // r = beta (v - y)
+                meet<1>(s_max, part, lane, m, scale, back);
+                const float2 sb = make_float2(back[0], back[0]);
+                if (part == 0) s_out[0] = back[0];
+                store_s(0, scale[0]);
+                store_s(1, scale[0]);
+                // r = beta (v - y), beta v before y is there
                 wait(kFullSv + (it & 1), (it >> 1) & 1);
                 wait(kFullV, par);
+                float2 bv[8];
+#pragma unroll
+                for (int t = 0; t < 8; t++) bv[t] = __fmul2_rn(pair_at(be + 2 * t), v_pair(t));
                 wait(kDoneY, par);
                 tc::fence_after();
-                tc::ld32(reinterpret_cast<uint32_t *>(y), tl + kColY + 32 * half);
+                tc::ld16(reinterpret_cast<uint32_t *>(y), tl + kColY + 16 * part);
                 m[0] = 0.f;
 #pragma unroll
-                for (int t = 0; t < 16; t++) {
-                    const float2 f = __fmul2_rn(pair_at(fy + 2 * t), make_float2(-sb, -sb));
-                    y[t] = __fmul2_rn(pair_at(be + 2 * t), __ffma2_rn(y[t], f, v_pair(t)));
+                for (int t = 0; t < 8; t++) {
+                    y[t] = __ffma2_rn(y[t], __fmul2_rn(pair_at(fy + 2 * t), sb), bv[t]);
                     m[0] = max_abs(m[0], y[t]);
                 }
-                meet<1>(s_max + 2 * kDV, half, lane, m, scale, back);
-                store_halves<16>(tl + kColY + 16 * half, tl + kColY + 32 + 16 * half, scale[0], [&](int t) { return y[t]; });
+                meet<1>(s_max + 4 * kDV, part, lane, m, scale, back);
+                store_halves<8>(tl + kColY + 8 * part, tl + kColY + 32 + 8 * part, scale[0], [&](int t) { return y[t]; });
+                if (part == 0) s_out[kDV] = back[0];
                 tc::wait_st();
                 tc::fence_before();
                 arrive(kGotR);
-                // u = inv r, and what of it is left at the block's end
+                // what of u = inv r is left at the block's end
                 wait(kDoneU, par);
                 tc::fence_after();
                 const float2 rb = make_float2(back[0], back[0]);
-                tc::ld32(reinterpret_cast<uint32_t *>(y), tl + kColU + 32 * half);
-                m[0] = m[1] = 0.f;
+                tc::ld16(reinterpret_cast<uint32_t *>(y), tl + kColU + 16 * part);
+                m[0] = 0.f;
 #pragma unroll
-                for (int t = 0; t < 16; t++) {
-                    y[t] = __fmul2_rn(y[t], __fmul2_rn(pair_at(ft + 2 * t), rb));
+                for (int t = 0; t < 8; t++) {
+                    y[t] = __fmul2_rn(y[t], __fmul2_rn(pair_at(fu + 2 * t), rb));
                     m[0] = max_abs(m[0], y[t]);
-                    m[1] = max_abs(m[1], __fmul2_rn(y[t], pair_at(fu + 2 * t)));
                 }
-                meet<2>(s_max, half, lane, m, scale, back);
-                store_halves<16>(tl + kColY + 16 * half, tl + kColY + 32 + 16 * half, scale[1], [&](int t) { return __fmul2_rn(y[t], pair_at(fu + 2 * t)); });
-                store_halves<16>(tl + kColU + 16 * half, tl + kColU + 32 + 16 * half, scale[0], [&](int t) { return y[t]; });
-                if (half == 0) s_back[(2 * (it & 1) + 1) * kDV + lane] = back[0];
+                meet<1>(s_max + 8 * kDV, part, lane, m, scale, back);
+                store_halves<8>(tl + kColU + 8 * part, tl + kColU + 32 + 8 * part, scale[0], [&](int t) { return y[t]; });
                 tc::wait_st();
                 tc::fence_before();
                 arrive(kGotU);
+                back[2] = back[0];
             }
-            wait(kDoneD, par);
+            wait(kDoneD + (part >> 1), par);
             tc::fence_after();
-            const float2 ub = make_float2(back[1], back[1]);
-            const float keep = V == kKda ? 0.f : sv[4 * kC];
+            const float2 ub = make_float2(back[2], back[2]);
+            const float keep = V == kKda ? 0.f : sv[3 * kC];
 #pragma unroll
-            for (int j1 = 0; j1 < 32; j1 += 8) {
+            for (int j1 = 0; j1 < 16; j1 += 8) {
                 float2 d[8];
-                tc::ld16(reinterpret_cast<uint32_t *>(d), tl + kColD + 64 * half + 2 * j1);
+                tc::ld16(reinterpret_cast<uint32_t *>(d), tl + kColD + 32 * part + 2 * j1);
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    const float2 kp = V == kKda ? pair_at(sv + 4 * kC + 64 * half + 2 * (j1 + j)) : make_float2(keep, keep);
+                    const float2 kp = V == kKda ? pair_at(sv + 3 * kC + 32 * part + 2 * (j1 + j)) : make_float2(keep, keep);
                     s[j1 + j] = __ffma2_rn(kp, s[j1 + j], __fmul2_rn(d[j], ub));
                 }
             }
         }
 #pragma unroll
-        for (int j = 0; j < 32; j++) {
+        for (int j = 0; j < 16; j++) {
             Sp[2 * j * kDV] = s[j].x;
             Sp[(2 * j + 1) * kDV] = s[j].y;
         }
