@@ -15,9 +15,9 @@ LIB = os.path.join(HERE, "libstepq.so")
 # memory; see stepq_pool_check_guards in include/stepq.h)
 LIB_CHECK = os.path.join(HERE, "libstepq_check.so")
 SOURCES = ["stepq_abi.cu", "stepq_kernels.cu", "stepq_serve_abi.cu", "stepq_plan.cu", "stepq_prompt.cu",
-           "stepq_prompt_blocks.cu", "stepq_beam.cu"]
+           "stepq_prompt_tiles.cu", "stepq_prompt_blocks.cu", "stepq_beam.cu"]
 HEADERS = ["stepq_internal.cuh", "stepq_device.cuh", "stepq_host.cuh", "stepq_serve.cuh", "stepq_mma.cuh",
-           "stepq_tcgen05.cuh"]
+           "stepq_tcgen05.cuh", "stepq_prompt_blocks.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -24,400 +24,13 @@
 
 #include "stepq_device.cuh"
 #include "stepq_mma.cuh"
-#include "stepq_serve.cuh"
+#include "stepq_prompt_blocks.cuh"
 #include "stepq_tcgen05.cuh"
 
 namespace stepq {
 namespace {
 
-using dev::ldsm4;
-using dev::ldsm4_t;
-using dev::mma16816;
-
-constexpr unsigned kFull = 0xffffffffu;
-constexpr int kC = kBlockTokens;
-constexpr int kTileBytes = kC * kDK * 2;    // one binary16 half of a [64][128] operand
-constexpr int kSquareBytes = kC * kC * 2 * 2;  // hi and lo of a [64][64] operand
-// per block and head, for the state: -beta c_t times the unscale of the K rows, beta,
-// unscale of the rows that make U (plain linear attention: what of each token
-// is left at the block's end, times the unscale of its K row), kept share of S
-constexpr int kStateFloats = 3 * kC + kDK;
-constexpr int kOutFloats = 2 * kC;          // for the output: unscale of the Q rows times c_t, of the P rows
 constexpr long long kWaitLimit = 1LL << 32;  // cycles, about two seconds
-
-// Byte of element (row, col) of an operand tile [64][128] (two halves of 64
-// columns) and of a [64][64] one: rows of 128 bytes whose 16-byte chunks are
-// permuted by the row, the layout the tensor cores read and in which eight rows
-// of one chunk lie in different banks.
-__device__ __forceinline__ int square_at(int row, int col) { return row * 128 + (((col >> 3) ^ row) & 7) * 16 + (col & 7) * 2; }
-__device__ __forceinline__ int tile_at(int row, int col) { return (col >> 6) * (kTileBytes / 2) + square_at(row, col & 63); }
-
-// The scratch of a launch over `blocks` blocks.
-struct Scratch {
-    int heads_k;  // heads the K and Q tiles are made for
-    int halves;   // binary16 halves of K and Q
-    size_t k, q, k2, inv, p, sv, ov, total;
-};
-
-__host__ __device__ Scratch scratch_of(int variant, int dtype, int heads, int share, long long blocks)
-{
-    Scratch s;
-    s.heads_k = variant == kKda ? heads : heads / share;
-    s.halves = variant == kKda || dtype == kF32 ? 2 : 1;
-    const size_t tiles = (size_t)blocks * s.heads_k * s.halves * kTileBytes, bh = (size_t)blocks * heads;
-    size_t o = 0;
-    s.k = o;   o += tiles;
-    s.q = o;   o += tiles;
-    s.k2 = o;  o += variant == kKda ? tiles : 0;
-    s.inv = o; o += variant == kLinear ? 0 : bh * kSquareBytes;
-    s.p = o;   o += bh * kSquareBytes;
-    s.sv = o;  o += bh * kStateFloats * 4;
-    s.ov = o;  o += bh * kOutFloats * 4;
-    s.total = o;
-    return s;
-}
-
-// Four consecutive elements.
-__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __half *p)
-{
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&v.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p)
-{
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xffff0000u));
-}
-
-__device__ __forceinline__ float warp_max(float m)
-{
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-    return m;
-}
-
-// One row of an operand (4 elements a lane) as scaled halves, into the tile in
-// shared memory and its image in the scratch; returns the row's unscale.
-template <int NP, bool EXACT>
-__device__ __forceinline__ float put_row(float4 x, int row, int l, char *tile, char *image)
-{
-    float scale = 1.f, back = 1.f;
-    if (!EXACT) {  // binary16 inputs are their own halves
-        const float m = warp_max(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-        dev::row_scale(m, &scale, &back);
-    }
-    uint32_t hi[2], lo[2];
-    dev::split_half(x.x * scale, x.y * scale, &hi[0], &lo[0]);
-    dev::split_half(x.z * scale, x.w * scale, &hi[1], &lo[1]);
-    const int at = tile_at(row, 4 * l);
-    const uint2 h = make_uint2(hi[0], hi[1]), o = make_uint2(lo[0], lo[1]);
-    *reinterpret_cast<uint2 *>(tile + at) = h;
-    *reinterpret_cast<uint2 *>(image + at) = h;
-    if (NP == 2) {
-        *reinterpret_cast<uint2 *>(tile + kTileBytes + at) = o;
-        *reinterpret_cast<uint2 *>(image + kTileBytes + at) = o;
-    }
-    return back;
-}
-
-// acc[j] = rows 16 m .. 16 m + 15 of A times rows 8 j .. of B transposed, for
-// the column tiles j < tiles (a multiple of 2): A and B operand tiles in
-// shared memory.
-template <int NP>
-__device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, const char *B, int m, int tiles)
-{
-    const int l = threadIdx.x & 31;
-    const uint32_t a0 = dev::smem_addr(A), b0 = dev::smem_addr(B);
-    const int arow = 16 * m + (l & 7) + ((l >> 3) & 1) * 8, acol = (l >> 4) * 8;  // of the A matrices
-    const int brow = (l & 7) + (l >> 4) * 8, bcol = ((l >> 3) & 1) * 8;           // of two column tiles
-#pragma unroll
-    for (int i = 0; i < kDK / 16; i++) {
-        uint32_t ah[4], al[4];
-        ldsm4(ah, a0 + tile_at(arow, 16 * i + acol));
-        if (NP == 2) ldsm4(al, a0 + kTileBytes + tile_at(arow, 16 * i + acol));
-        uint32_t b[kC / 8][2];
-#pragma unroll
-        for (int j = 0; j < kC / 8; j += 2)
-            if (j < tiles) ldsm4(b[j], b[j + 1], b0 + tile_at(8 * j + brow, 16 * i + bcol));
-        if (NP == 2) {
-#pragma unroll
-            for (int j = 0; j < kC / 8; j++)
-                if (j < tiles) mma16816(acc[j], al[0], al[1], al[2], al[3], b[j][0], b[j][1]);
-        }
-#pragma unroll
-        for (int j = 0; j < kC / 8; j++)
-            if (j < tiles) mma16816(acc[j], ah[0], ah[1], ah[2], ah[3], b[j][0], b[j][1]);
-        if (NP == 2) {
-#pragma unroll
-            for (int j = 0; j < kC / 8; j += 2)
-                if (j < tiles) ldsm4(b[j], b[j + 1], b0 + kTileBytes + tile_at(8 * j + brow, 16 * i + bcol));
-#pragma unroll
-            for (int j = 0; j < kC / 8; j++)
-                if (j < tiles) mma16816(acc[j], ah[0], ah[1], ah[2], ah[3], b[j][0], b[j][1]);
-        }
-    }
-}
-
-constexpr int kLd = kC + 4;  // row of a [64][64] fp32 matrix in shared memory
-
-// The lower triangle of a [64][64] fp32 matrix, rows as scaled halves, into the
-// scratch; the rows' unscales into back[].  Columns past the row's block of 16
-// are not written (and not read).
-__device__ __forceinline__ void put_square(const float *x, char *image, float *back)
-{
-    const int row = threadIdx.x >> 2, part = threadIdx.x & 3;  // 256 threads: 16 columns each
-    const bool inside = part <= row >> 4;
-    float v[16], m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (inside) y = *reinterpret_cast<const float4 *>(x + row * kLd + 16 * part + i);
-        v[i] = y.x; v[i + 1] = y.y; v[i + 2] = y.z; v[i + 3] = y.w;
-        m = fmaxf(fmaxf(fmaxf(m, fabsf(y.x)), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
-    }
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-    float scale, b;
-    dev::row_scale(m, &scale, &b);
-    if (part == 0) back[row] = b;
-    if (!inside) return;
-    uint32_t hi[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) dev::split_half(v[2 * i] * scale, v[2 * i + 1] * scale, &hi[i], &lo[i]);
-#pragma unroll
-    for (int e = 0; e < 2; e++) {
-        const int at = square_at(row, 16 * part + 8 * e);
-        *reinterpret_cast<uint4 *>(image + at) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-        *reinterpret_cast<uint4 *>(image + kSquareBytes / 2 + at) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
-    }
-}
-
-// inv = (I + A)^-1 for the strictly lower triangular A [64][64] (both in shared
-// memory, 256 threads): the four diagonal blocks of 16 by substitution, then
-// twice the rule inv_21 = -inv_22 A_21 inv_11 for the blocks below.  tmp: room
-// for a [32][33] matrix.  Only the lower triangle of inv (and the rest of its
-// diagonal blocks of 16) is written.
-__device__ void invert_lower(const float *A, float *inv, float *tmp)
-{
-    const int tid = threadIdx.x;
-    if (tid < kC) {
-        const int b = tid & ~15, j = tid & 15;
-        float x[16];
-#pragma unroll
-        for (int r = 0; r < 16; r++) {
-            float s = 0.f;
-#pragma unroll
-            for (int m = 0; m < r; m++) s = fmaf(A[(b + r) * kLd + b + m], x[m], s);
-            x[r] = r < j ? 0.f : (r == j ? 1.f : -s);
-            inv[(b + r) * kLd + b + j] = x[r];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 16; h <= 32; h *= 2) {
-        // 64 / 2h pairs of h x h outputs, h h / 2 ... : 4 (h = 32) or 2 rows of one column a thread
-        const int rows = h / 8;
-        const int j = tid & (h - 1), i0 = (tid / h) % (h / rows) * rows, pair = tid / (h * (h / rows));
-        const int lo = 2 * h * pair, hi = lo + h;
-        float x[4] = {};
-        for (int m = 0; m < h; m++) {
-            const float t = inv[(lo + m) * kLd + lo + j];
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (e < rows) x[e] = fmaf(A[(hi + i0 + e) * kLd + lo + m], m >= j ? t : 0.f, x[e]);
-        }
-        float *X = tmp + pair * h * (h + 1);
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (e < rows) X[(i0 + e) * (h + 1) + j] = x[e];
-        __syncthreads();
-        float y[4] = {};
-        for (int m = 0; m < h; m++) {
-            const float t = X[m * (h + 1) + j];
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (e < rows) y[e] = fmaf(m <= i0 + e ? inv[(hi + i0 + e) * kLd + hi + m] : 0.f, t, y[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            if (e < rows) inv[(hi + i0 + e) * kLd + lo + j] = -y[e];
-        __syncthreads();
-    }
-}
-
-// out = X Y for lower-triangular X and Y [64][64] (shared memory, 256 threads;
-// a thread makes 4 x 4 outputs).  The blocks of 16 x 16 on and below the
-// diagonal are written.
-__device__ void lower_product(const float *X, const float *Y, float *out)
-{
-    const int i0 = 4 * (threadIdx.x >> 4), j0 = 4 * (threadIdx.x & 15);
-    if ((j0 & ~15) > i0) return;
-    float acc[4][4] = {};
-    // both are zero above their diagonals: inner indices from the columns' block to the rows'
-    for (int m = j0 & ~3; m < i0 + 4; m += 4) {
-        float4 x[4], y[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            x[e] = *reinterpret_cast<const float4 *>(X + (i0 + e) * kLd + m);
-            y[e] = *reinterpret_cast<const float4 *>(Y + (m + e) * kLd + j0);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-#pragma unroll
-            for (int d = 0; d < 4; d++) {
-                acc[e][0] = fmaf(xs[d], y[d].x, acc[e][0]);
-                acc[e][1] = fmaf(xs[d], y[d].y, acc[e][1]);
-                acc[e][2] = fmaf(xs[d], y[d].z, acc[e][2]);
-                acc[e][3] = fmaf(xs[d], y[d].w, acc[e][3]);
-            }
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; e++) *reinterpret_cast<float4 *>(out + (i0 + e) * kLd + j0) = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
-}
-
-// What a tile kernel's CTA works on: a block of a live request.
-struct Block {
-    int b, r, t0, n;  // block of this launch, request, first token row, tokens
-};
-
-__device__ __forceinline__ bool find_block(const PromptArgs &a, int first_block, int b, Block *k)
-{
-    const int g = first_block + b;
-    k->b = b;
-    k->r = a.p.block_request[g];
-    if (k->r < 0 || a.p.live[k->r] < 0) return false;
-    const int end = a.p.starts[k->r + 1];
-    k->t0 = a.p.starts[k->r] + a.p.block_first[g];
-    k->n = min(kC, end - k->t0);
-    return true;
-}
-
-// ---------------------------------------------------------------------------
-// The blocks' own products, one gate a head.  A CTA takes a block and a query /
-// key head: K K^T and Q K^T on the tensor cores (warps 0-3 and 4-7, 16 rows
-// each), then for each value head of the group the decays, the inverse and P.
-// ---------------------------------------------------------------------------
-template <class T, int V, int NP>
-__global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_block, Scratch sc)
-{
-    extern __shared__ __align__(1024) char smem[];
-    __shared__ float ek[kC], eq[kC], s_alpha[kC], s_beta[kC], s_left[kC], s_inv[kC], s_p[kC];
-    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
-    const int heads_k = a.heads / a.share;
-    Block k;
-    const int hq = blockIdx.x % heads_k;
-    if (!find_block(a, first_block, blockIdx.x / heads_k, &k)) return;
-    char *tk = smem, *tq = smem + NP * kTileBytes;
-    {
-        const size_t at = ((size_t)k.b * heads_k + hq) * NP * kTileBytes;
-        char *ik = reinterpret_cast<char *>(a.scratch) + sc.k + at, *iq = reinterpret_cast<char *>(a.scratch) + sc.q + at;
-        const T *kg = static_cast<const T *>(a.k) + hq * kDK, *qg = static_cast<const T *>(a.q) + hq * kDK;
-        constexpr bool exact = sizeof(T) == 2 && !std::is_same<T, __nv_bfloat16>::value;
-#pragma unroll
-        for (int i = 0; i < kC / 8; i++) {
-            const int row = 8 * w + i;
-            float4 xk = make_float4(0.f, 0.f, 0.f, 0.f), xq = xk;
-            if (row < k.n) {
-                xk = load4(kg + (long long)(k.t0 + row) * a.stride_k + 4 * l);
-                xq = load4(qg + (long long)(k.t0 + row) * a.stride_q + 4 * l);
-            }
-            const float bk = put_row<NP, exact>(xk, row, l, tk, ik), bq = put_row<NP, exact>(xq, row, l, tq, iq);
-            if (l == 0) {
-                ek[row] = bk;
-                eq[row] = bq;
-            }
-        }
-    }
-    __syncthreads();
-    const int m = w & 3;  // rows 16 m + g, + 8
-    const bool is_q = w >= 4;
-    float acc[kC / 8][4] = {};
-    if (is_q || V != kLinear) rows_product<NP>(acc, is_q ? tq : tk, tk, m, 2 * m + 2);
-    {
-        const float r0 = (is_q ? eq : ek)[16 * m + g], r1 = (is_q ? eq : ek)[16 * m + g + 8];
-#pragma unroll
-        for (int j = 0; j < kC / 8; j++) {
-            const float c0 = ek[8 * j + 2 * c], c1 = ek[8 * j + 2 * c + 1];
-            acc[j][0] *= r0 * c0; acc[j][1] *= r0 * c1; acc[j][2] *= r1 * c0; acc[j][3] *= r1 * c1;
-        }
-    }
-    // the tiles are done with: their room holds the fp32 matrices
-    float *sD = reinterpret_cast<float *>(smem), *sA = sD + kC * kLd, *sP = sA + kC * kLd, *sI = sP + kC * kLd;
-    for (int v = 0; v < a.share; v++) {
-        const int h = hq * a.share + v;
-        __syncthreads();
-        if (tid < kC) {
-            const bool in = tid < k.n;
-            s_alpha[tid] = in ? a.alpha[(long long)(k.t0 + tid) * a.heads + h] : 1.f;
-            s_beta[tid] = in ? a.beta[(long long)(k.t0 + tid) * a.heads + h] : 0.f;
-        }
-        __syncthreads();
-        {
-            // decay_ts: column s, 16 rows a thread
-            const int s = tid & (kC - 1), seg = 16 * (tid / kC);
-            float p = 1.f;
-            for (int r = s + 1; r < seg; r++) p *= s_alpha[r];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                const int t = seg + i;
-                if (t > s) p *= s_alpha[t];
-                sD[t * kLd + s] = t >= s ? p : 0.f;
-            }
-        }
-        __syncthreads();
-        {
-            float *dst = is_q ? sP : sA;
-            const int t0 = 16 * m + g, t1 = t0 + 8;
-            const float b0 = is_q ? 1.f : s_beta[t0], b1 = is_q ? 1.f : s_beta[t1];
-            if (is_q || V != kLinear) {
-#pragma unroll
-                for (int j = 0; j < kC / 8; j++) {
-                    if (j >= 2 * m + 2) continue;
-                    const int s = 8 * j + 2 * c;
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const bool in0 = is_q ? s + e <= t0 : s + e < t0, in1 = is_q ? s + e <= t1 : s + e < t1;
-                        dst[t0 * kLd + s + e] = in0 ? acc[j][e] * sD[t0 * kLd + s + e] * b0 : 0.f;
-                        dst[t1 * kLd + s + e] = in1 ? acc[j][2 + e] * sD[t1 * kLd + s + e] * b1 : 0.f;
-                    }
-                }
-            }
-        }
-        const size_t bh = (size_t)k.b * a.heads + h;
-        float *sv = reinterpret_cast<float *>(a.scratch + sc.sv) + bh * kStateFloats;
-        float *ov = reinterpret_cast<float *>(a.scratch + sc.ov) + bh * kOutFloats;
-        const float a0 = s_alpha[0];
-        if (tid < kC) {
-            const float ct = sD[tid * kLd] * a0;
-            sv[tid] = -s_beta[tid] * ct * ek[tid];
-            sv[kC + tid] = s_beta[tid];
-            // what of the token is left at the block's end, times the unscale of its K row in the update
-            s_left[tid] = sD[(kC - 1) * kLd + tid] * ek[tid];
-            ov[tid] = ct * eq[tid];
-            if (tid == 0) sv[3 * kC] = sD[(kC - 1) * kLd] * a0;
-        }
-        __syncthreads();
-        float *out = sP;
-        if (V != kLinear) {
-            invert_lower(sA, sI, sD);
-            lower_product(sP, sI, sA);
-            __syncthreads();
-            out = sA;
-        }
-        put_square(out, reinterpret_cast<char *>(a.scratch) + sc.p + bh * kSquareBytes, s_p);
-        if (V != kLinear) put_square(sI, reinterpret_cast<char *>(a.scratch) + sc.inv + bh * kSquareBytes, s_inv);
-        __syncthreads();
-        if (tid < kC) {
-            sv[2 * kC + tid] = V == kLinear ? s_left[tid] : s_inv[tid] * s_left[tid];
-            ov[kC + tid] = s_p[tid];
-        }
-    }
-}
 
 // ---------------------------------------------------------------------------
 // The walk over a request's blocks: one CTA a state, all products on the
@@ -902,16 +515,6 @@ int launch_blocks(const PromptArgs &a)
 }
 
 template <class T, int V, int NP>
-cudaError_t launch_tiles(const PromptArgs &a, int first, int n, const Scratch &sc, cudaStream_t s)
-{
-    const int dyn = std::max(2 * NP * kTileBytes, 4 * kC * kLd * 4);
-    cudaError_t e = cudaFuncSetAttribute(k_block_tiles<T, V, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
-    if (e != cudaSuccess) return e;
-    k_block_tiles<T, V, NP><<<(unsigned)n * (unsigned)(a.heads / a.share), 256, dyn, s>>>(a, first, sc);
-    return cudaGetLastError();
-}
-
-template <class T, int V, int NP>
 cudaError_t launch_walk(const PromptArgs &a, int first, int n, const Scratch &sc, cudaStream_t s)
 {
     using W = Walk<T, V, NP>;
@@ -928,7 +531,7 @@ cudaError_t launch_t(const PromptArgs &a, cudaStream_t s)
     const Scratch sc = scratch_of(a.variant, a.dtype, a.heads, a.share, step);
     for (int first = 0; first < a.p.blocks; first += step) {
         const int n = std::min(step, a.p.blocks - first);
-        cudaError_t e = launch_tiles<T, V, NP>(a, first, n, sc, s);
+        cudaError_t e = launch_block_tiles(a, first, n, sc, s);
         if (e != cudaSuccess) return e;
         e = launch_walk<T, V, NP>(a, first, n, sc, s);
         if (e != cudaSuccess) return e;
@@ -942,7 +545,7 @@ cudaError_t launch_v(const PromptArgs &a, cudaStream_t s)
     constexpr int NP = sizeof(T) == 4 ? 2 : 1;
     switch (a.variant) {
         case kGdn: return launch_t<T, kGdn, NP>(a, s);
-        case kKda: return launch_prompt_steps(a, s);
+        case kKda: return launch_t<T, kKda, 2>(a, s);
         default: return launch_t<T, kLinear, NP>(a, s);
     }
 }
@@ -951,7 +554,7 @@ cudaError_t launch_v(const PromptArgs &a, cudaStream_t s)
 
 size_t prompt_scratch_bytes(const PromptArgs &a)
 {
-    if (a.p.blocks == 0 || a.variant == kKda) return 0;
+    if (a.p.blocks == 0) return 0;
     return scratch_of(a.variant, a.dtype, a.heads, a.share, launch_blocks(a)).total;
 }
 
