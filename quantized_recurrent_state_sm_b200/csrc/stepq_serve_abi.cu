@@ -23,16 +23,22 @@ namespace {
 
 size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// A device tensor of this call: as check_dev, and on the current device.
+// A device tensor of this call: non-null, aligned, and memory of the current
+// device (one query a tensor; these calls are short).
 stepq_status check_here(const void *ptr, const char *name, size_t align)
 {
-    stepq_status st = check_dev(ptr, name, align);
-    if (st != STEPQ_OK) return st;
+    if (!ptr) return fail(STEPQ_ERR_INVALID_ARG, "%s is NULL", name);
+    if (reinterpret_cast<uintptr_t>(ptr) % align) return fail(STEPQ_ERR_INVALID_ARG, "%s is not %zu-byte aligned", name, align);
     cudaPointerAttributes at{};
     int dev = 0;
     cudaError_t e = cudaPointerGetAttributes(&at, ptr);
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, name);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return fail(STEPQ_ERR_INVALID_ARG, "%s: cannot query pointer (%s)", name, cudaGetErrorString(e));
+    }
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
+        return fail(STEPQ_ERR_INVALID_ARG, "%s is not device memory", name);
     if (at.type == cudaMemoryTypeDevice && at.device != dev)
         return fail(STEPQ_ERR_INVALID_ARG, "%s is on device %d, the current device is %d", name, at.device, dev);
     return STEPQ_OK;

@@ -149,8 +149,9 @@ def _check(status: int):
 
 
 def _stream_ptr(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return C.c_void_p(s.cuda_stream)
+    if stream is None:  # the raw handle: making a Stream object costs more than a small launch
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return C.c_void_p(stream.cuda_stream)
 
 
 def _dev(t: torch.Tensor, name: str, shape) -> C.c_void_p:
@@ -287,8 +288,7 @@ class PackedStatePool:
         (state r of request r), or with by_slot [batch, heads, 128, 128]."""
         rows = self.batch if by_slot else plan.requests
         self._sync_stream()
-        _check(lib.stepq_pack_requests(self._h, C.byref(plan._desc), C.c_void_p(plan.buffer.data_ptr()), plan.nbytes,
-                                       _dev(S, "S", (rows, self.heads, DK, DV)), int(by_slot)))
+        _check(lib.stepq_pack_requests(self._h, *plan._args, _dev(S, "S", (rows, self.heads, DK, DV)), int(by_slot)))
 
     def reorder(self, parents: torch.Tensor, first: int = 0):
         """Reorder packed states inside groups, in place: with parents [groups,
@@ -423,12 +423,14 @@ class RequestPlan:
         self.requests, self.tokens = int(requests), int(tokens)
         self.n_slots = self.requests if slots is None else int(slots)
         self.max_length = self.tokens
+        self._prompts = {}  # descriptor and scratch size of the prompts run over this plan, by their sizes
         self._desc = PlanDesc(self.requests, self.tokens, self.n_slots)
         r = PlanRegions()
         _check(lib.stepq_plan_layout(C.byref(self._desc), C.byref(r)))
         self.nbytes, self.blocks = int(r.total), int(r.blocks)
         dev = torch.device("cuda") if device is None else torch.device(device)
         self.buffer = torch.empty(max(self.nbytes, 16), dtype=torch.uint8, device=dev)
+        self._args = C.byref(self._desc), C.c_void_p(self.buffer.data_ptr()), self.nbytes
         ints = self.buffer[:self.nbytes].view(torch.int32)
 
         def view(offset, n):
@@ -448,19 +450,18 @@ class RequestPlan:
         slots of -1 are served and which is updated; max_length: an upper bound
         of the lengths (default: the plan's tokens)."""
         n = lengths.shape[0] if isinstance(lengths, torch.Tensor) and lengths.dim() == 1 else -1
-        ptr = [_dev_any(lengths, "lengths", torch.int32, (max(n, 0),))]
-        for t, name in ((contexts, "contexts"), (slots, "slots")):
-            ptr.append(None if t is None else _dev_any(t, name, torch.int32, (n,)))
-        ptr.append(None if busy is None else _dev_any(busy, "busy", torch.uint8, (self.n_slots,)))
         bound = self.tokens if max_length is None else int(max_length)
-        _check(lib.stepq_plan_build(C.byref(self._desc), C.c_void_p(self.buffer.data_ptr()), self.nbytes, n, *ptr, bound,
-                                    _stream_ptr()))
+        _check(lib.stepq_plan_build(*self._args, n, _dev_any(lengths, "lengths", torch.int32, (max(n, 0),)),
+                                    None if contexts is None else _dev_any(contexts, "contexts", torch.int32, (n,)),
+                                    None if slots is None else _dev_any(slots, "slots", torch.int32, (n,)),
+                                    None if busy is None else _dev_any(busy, "busy", torch.uint8, (self.n_slots,)),
+                                    bound, _stream_ptr()))
         self.max_length = bound
         return self
 
     def check(self):
         """Synchronise the current stream and raise if the plan refused a request."""
-        _check(lib.stepq_plan_check(C.byref(self._desc), C.c_void_p(self.buffer.data_ptr()), self.nbytes, _stream_ptr()))
+        _check(lib.stepq_plan_check(*self._args, _stream_ptr()))
 
 
 def _rows(t: torch.Tensor, name: str, dtype, tokens: int, heads: int):
@@ -492,20 +493,24 @@ def prompt(variant: int, plan: RequestPlan, q: torch.Tensor, k: torch.Tensor, v:
     T, Hk, H, dt = plan.tokens, q.shape[1], v.shape[1], q.dtype
     (qp, qs), (kp, ks) = _rows(q, "q", dt, T, Hk), _rows(k, "k", dt, T, Hk)
     vp, vs = _rows(v, "v", dt, T, H)
-    d = PromptDesc(variant, _DTYPES[dt], H, Hk, DK, DV, plan.max_length, int(by_slot), qs, ks, vs)
     ap = _dev(alpha, "alpha", (T, H, DK) if variant == KDA else (T, H))
     bp = _dev(beta, "beta", (T, H))
     Sp = _dev(S, "S", (plan.n_slots if by_slot else plan.requests, H, DK, DV))
     if out is None:
         out = torch.empty((T, H, DV), dtype=dt, device=q.device)
     op = _dev_any(out, "out", dt, (T, H, DV))
-    need = lib.stepq_prompt_scratch_bytes(C.byref(plan._desc), C.byref(d))
-    if need == C.c_size_t(-1).value:
-        _check(ERR_INVALID_ARG)
+    key = (variant, dt, H, Hk, plan.max_length, by_slot, qs, ks, vs)
+    if key not in plan._prompts:
+        d = PromptDesc(variant, _DTYPES[dt], H, Hk, DK, DV, plan.max_length, int(by_slot), qs, ks, vs)
+        need = lib.stepq_prompt_scratch_bytes(C.byref(plan._desc), C.byref(d))
+        if need == C.c_size_t(-1).value:
+            _check(ERR_INVALID_ARG)
+        plan._prompts[key] = d, need
+    d, need = plan._prompts[key]
     # from torch's allocator, so that calls on several streams or in several graphs have their own
     scratch = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    _check(lib.stepq_prompt(C.byref(plan._desc), C.c_void_p(plan.buffer.data_ptr()), plan.nbytes, C.byref(d), qp, kp, vp, ap,
-                            bp, Sp, op, C.c_void_p(scratch.data_ptr()) if need else None, need, _stream_ptr()))
+    _check(lib.stepq_prompt(*plan._args, C.byref(d), qp, kp, vp, ap, bp, Sp, op,
+                            C.c_void_p(scratch.data_ptr()) if need else None, need, _stream_ptr()))
     return out
 
 
@@ -528,13 +533,11 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: int | None = None
     if G > 1 and B > 1 and logits.stride(0) != B * stride:
         raise ValueError("logits: rows must be evenly spaced")
     dev = logits.device
-    out = (torch.empty((G, n), dtype=torch.float32, device=dev), torch.empty((G, n), dtype=torch.int32, device=dev),
-           torch.empty((G, n), dtype=torch.int32, device=dev)) if n >= 0 else ()
-    if not out:
-        raise ValueError("n must be positive")
     need = lib.stepq_beam_scratch_bytes(G, B, V, n)
     if need == 0:
         _check(ERR_INVALID_ARG)
+    best, parents, tokens = torch.empty((3, G, n), dtype=torch.int32, device=dev).unbind(0)
+    out = best.view(torch.float32), parents, tokens
     scratch = torch.empty(need, dtype=torch.uint8, device=dev)
     _check(lib.stepq_beam_select(G, B, V, n, _DTYPES[logits.dtype], C.c_void_p(logits.data_ptr()), stride, sp,
                                  *(C.c_void_p(t.data_ptr()) for t in out), C.c_void_p(scratch.data_ptr()), need, _stream_ptr()))
