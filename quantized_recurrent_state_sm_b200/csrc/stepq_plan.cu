@@ -13,7 +13,7 @@ namespace stepq {
 namespace {
 
 constexpr int kPlanThreads = 512;
-constexpr int kPlanRange = 2048;  // entries of a CTA
+constexpr int kPlanRange = 2048;  // entries of a CTA, and requests of a turn
 constexpr int kPer = kPlanRange / kPlanThreads;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr unsigned kSat = 1u << 30;  // sums stop here (the largest token count is 2^28)
@@ -22,39 +22,44 @@ constexpr unsigned kSat = 1u << 30;  // sums stop here (the largest token count 
 // group them in any way.
 __device__ __forceinline__ unsigned sat_add(unsigned a, unsigned b) { return min(a + b, kSat); }
 
-// Length of request r as the token rows see it: at least 0, and small enough to add.
-__device__ __forceinline__ unsigned length_of(const PlanArgs &a, int r)
-{
-    const int n = a.lengths[r];
-    return n <= 0 ? 0u : min((unsigned)n, kSat);
-}
+// A length as the token rows see it: at least 0, and small enough to add.
+__device__ __forceinline__ unsigned length_of(int n) { return n <= 0 ? 0u : min((unsigned)n, kSat); }
 
 __device__ __forceinline__ unsigned blocks_of(unsigned len) { return (len + kBlockTokens - 1) / kBlockTokens; }
 
-struct Pair {
-    unsigned tokens, blocks;
+struct Sums {
+    unsigned tokens, blocks, fresh;  // fresh: requests that ask for a slot
 };
 
-__device__ __forceinline__ Pair add(Pair x, Pair y) { return {sat_add(x.tokens, y.tokens), x.blocks + y.blocks}; }
+__device__ __forceinline__ Sums add(Sums x, Sums y) { return {sat_add(x.tokens, y.tokens), x.blocks + y.blocks, x.fresh + y.fresh}; }
+
+struct Shared {
+    Sums sums[kPlanThreads / 32];
+    int maxima[kPlanThreads / 32];
+    int mark[kPlanRange], from[kPlanRange];
+    int flags;
+    unsigned rows, blocks;
+};
 
 // Exclusive sum over the CTA's threads; *total gets the sum of all.
-__device__ Pair block_scan(Pair v, Pair *sm, Pair *total)
+__device__ Sums block_scan(Sums v, Shared &sm, Sums *total)
 {
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
-    Pair inc = v;
+    Sums inc = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        Pair o = {__shfl_up_sync(kFull, inc.tokens, d), __shfl_up_sync(kFull, inc.blocks, d)};
+        const Sums o = {__shfl_up_sync(kFull, inc.tokens, d), __shfl_up_sync(kFull, inc.blocks, d), __shfl_up_sync(kFull, inc.fresh, d)};
         if (l >= d) inc = add(o, inc);
     }
-    if (l == 31) sm[w] = inc;
-    Pair ex = {__shfl_up_sync(kFull, inc.tokens, 1), __shfl_up_sync(kFull, inc.blocks, 1)};
-    if (l == 0) ex = {0, 0};
+    if (l == 31) sm.sums[w] = inc;
+    Sums ex = {__shfl_up_sync(kFull, inc.tokens, 1), __shfl_up_sync(kFull, inc.blocks, 1), __shfl_up_sync(kFull, inc.fresh, 1)};
+    if (l == 0) ex = {0, 0, 0};
     __syncthreads();
-    Pair base = {0, 0}, all = {0, 0};
+    Sums base = {0, 0, 0}, all = base;
+#pragma unroll
     for (int i = 0; i < kPlanThreads / 32; i++) {
         if (i == w) base = all;
-        all = add(all, sm[i]);
+        all = add(all, sm.sums[i]);
     }
     __syncthreads();
     *total = all;
@@ -82,192 +87,261 @@ __device__ void scan_max(int *v, int *sm)
     for (int i = 0; i < kPer; i++) v[i] = max(v[i], before);
 }
 
+// Four consecutive lengths (0 past the batch).
+__device__ __forceinline__ void four(const int *p, int r, int n, int *x)
+{
+#pragma unroll
+    for (int i = 0; i < kPer; i++) x[i] = r + i < n ? p[r + i] : 0;
+}
+
+// Which of 16 bytes from `at` on are zero, as bits.
+__device__ __forceinline__ unsigned zero_bytes(const uint8_t *p, int at, int n)
+{
+    unsigned z = 0;
+    if (at + 16 <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p + at);
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 16; i++) z |= (unsigned)(((w[i >> 2] >> (8 * (i & 3))) & 255) == 0) << i;
+    } else {
+        for (int i = 0; i < 16; i++)
+            if (at + i < n && p[at + i] == 0) z |= 1u << i;
+    }
+    return z;
+}
+
 // Slots, live flags and starts of all requests, and the plan's head.
-__device__ void resolve(const PlanArgs &a, int r0, int r1, Pair at, Pair *sm, int *flags)
+__device__ void resolve(const PlanArgs &a, Shared &sm)
 {
     const PlanView &p = a.p;
     const int tid = threadIdx.x;
-    __shared__ unsigned rows_used, blocks_used;
-    if (tid == 0) { *flags = 0; rows_used = 0; blocks_used = 0; }
-    __syncthreads();
-    // A request whose tokens pass the capacity ends the batch: it and all after
-    // it have no tokens.
-    unsigned need = 0, rows = 0, blocks = 0;
-    int bad = 0;
-    for (int r = r0; r < r1; r++) {
-        const unsigned len = length_of(a, r);
-        if (a.lengths[r] < 0) bad |= kPlanBadLength;
-        const Pair end = add(at, {len, blocks_of(len)});
-        const bool fits = end.tokens <= (unsigned)p.tokens;
-        if (fits) {
-            if (r == 0) p.starts[0] = p.block_starts[0] = 0;
-            p.starts[r + 1] = (int)end.tokens;
-            p.block_starts[r + 1] = (int)end.blocks;
-            rows = end.tokens;
-            blocks = end.blocks;
-        } else {
-            if (r == 0) p.starts[0] = p.block_starts[0] = 0;
-            p.starts[r + 1] = -1;  // set to the last end below
-            bad |= kPlanTooMany;
-        }
-        const bool tokens = fits && len > 0;
-        const int ctx = a.contexts ? a.contexts[r] : 0;
-        int s = a.slots ? a.slots[r] : r;
-        bool take = tokens;
-        if (tokens && a.lengths[r] > a.max_length) { bad |= kPlanBadLength; take = false; }
-        if (s < 0 || s >= p.slots) {
-            if (take && s == -1 && ctx == 0 && a.busy) {
-                need++;
-                s = -2;  // gets a free slot below
-            } else {
-                if (take) bad |= kPlanBadSlot;
-                take = false;
-                s = -1;
-            }
-        }
-        p.slot[r] = s;
-        p.live[r] = take ? s : -1;
-        p.fresh[r] = ctx == 0;
-        if (take && s >= 0 && a.slots) p.owner[s] = 0x7fffffff;
-        at = end;
+    if (tid == 0) {
+        sm.flags = 0;
+        sm.rows = sm.blocks = 0;
+        p.starts[0] = p.block_starts[0] = 0;
     }
+    __syncthreads();
+    Sums carry = {0, 0, 0};
+    for (int r0 = 0; r0 < a.n; r0 += kPlanRange) {
+        const int r = r0 + kPer * tid;
+        int n[kPer], ctx[kPer] = {}, slot[kPer], ask[kPer];
+        unsigned len[kPer];
+        four(a.lengths, r, a.n, n);
+        if (a.contexts) four(a.contexts, r, a.n, ctx);
+        if (a.slots) four(a.slots, r, a.n, slot);
+        Sums mine = {0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            if (!a.slots) slot[i] = r + i;
+            len[i] = length_of(n[i]);
+            // a new request that asks for a free slot (whether its tokens fit is not known yet:
+            // the requests that do not fit are the last, so they take nobody's rank)
+            ask[i] = len[i] > 0 && n[i] <= a.max_length && slot[i] == -1 && ctx[i] == 0 && a.busy != nullptr;
+            mine = add(mine, {len[i], blocks_of(len[i]), (unsigned)ask[i]});
+        }
+        Sums all, at = add(carry, block_scan(mine, sm, &all));
+        carry = add(carry, all);
+        unsigned rows = 0, blocks = 0;
+        int bad = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            if (r + i >= a.n) continue;
+            const unsigned before = at.fresh;
+            at = add(at, {len[i], blocks_of(len[i]), (unsigned)ask[i]});
+            // a request whose tokens pass the capacity ends the batch: it and all after it have none
+            const bool fits = at.tokens <= (unsigned)p.tokens;
+            p.starts[r + i + 1] = fits ? (int)at.tokens : -1;  // -1: set to the last end below
+            p.block_starts[r + i + 1] = (int)at.blocks;
+            if (fits) {
+                rows = at.tokens;
+                blocks = at.blocks;
+            } else {
+                bad |= kPlanTooMany;
+            }
+            if (n[i] < 0) bad |= kPlanBadLength;
+            bool take = fits && len[i] > 0;
+            if (take && n[i] > a.max_length) {
+                bad |= kPlanBadLength;
+                take = false;
+            }
+            int s = slot[i];
+            if (s < 0 || s >= p.slots) {
+                if (take && ask[i]) {
+                    s = -2 - (int)before;  // gets the free slot of this rank below
+                } else {
+                    if (take) bad |= kPlanBadSlot;
+                    take = false;
+                    s = -1;
+                }
+            }
+            p.slot[r + i] = s;
+            p.live[r + i] = take && s >= 0 ? s : -1;
+            p.fresh[r + i] = ctx[i] == 0;
+            if (take && s >= 0 && a.slots) p.owner[s] = 0x7fffffff;
+        }
+        if (rows) atomicMax(&sm.rows, rows);
+        if (blocks) atomicMax(&sm.blocks, blocks);
+        if (bad) atomicOr(&sm.flags, bad);
+    }
+    __syncthreads();
+    const int rows = (int)sm.rows, blocks = (int)sm.blocks;
+    if (sm.flags & kPlanTooMany)
+        for (int r = tid; r < a.n; r += kPlanThreads)
+            if (p.starts[r + 1] < 0) {
+                p.starts[r + 1] = rows;
+                p.block_starts[r + 1] = blocks;
+            }
     for (int r = a.n + tid; r < p.requests; r += kPlanThreads) {
+        p.starts[r + 1] = rows;
+        p.block_starts[r + 1] = blocks;
         p.slot[r] = -1;
         p.live[r] = -1;
         p.fresh[r] = 0;
-        p.starts[r + 1] = -1;
     }
-    if (a.n == 0 && tid == 0) p.starts[0] = p.block_starts[0] = 0;
-    if (rows) atomicMax(&rows_used, rows);
-    if (blocks) atomicMax(&blocks_used, blocks);
-    if (bad) atomicOr(flags, bad);
-    Pair all;
-    Pair rank = block_scan({need, 0}, sm, &all);  // orders the writes above, too
-    for (int r = tid; r < p.requests; r += kPlanThreads)
-        if (p.starts[r + 1] < 0) {
-            p.starts[r + 1] = (int)rows_used;
-            p.block_starts[r + 1] = (int)blocks_used;
-        }
     if (a.slots) {
         // a slot named twice belongs to the first request with tokens
-        for (int r = r0; r < r1; r++)
-            if (p.live[r] >= 0) atomicMin(&p.owner[p.live[r]], r);
+        for (int r0 = tid; r0 < a.n; r0 += 4 * kPlanThreads) {
+            int s[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) s[i] = r0 + i * kPlanThreads < a.n ? p.live[r0 + i * kPlanThreads] : -1;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (s[i] >= 0) atomicMin(&p.owner[s[i]], r0 + i * kPlanThreads);
+        }
         __syncthreads();
-        for (int r = r0; r < r1; r++) {
-            const int s = p.live[r];
-            if (s < 0) continue;
-            if (atomicAdd(&p.owner[s], 0) != r) {
-                p.live[r] = -1;
-                atomicOr(flags, kPlanSlotTwice);
-            } else if (a.busy) {
-                a.busy[s] = 1;
+        for (int r0 = tid; r0 < a.n; r0 += 4 * kPlanThreads) {
+            int s[4], o[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) s[i] = r0 + i * kPlanThreads < a.n ? p.live[r0 + i * kPlanThreads] : -1;
+#pragma unroll
+            for (int i = 0; i < 4; i++) o[i] = s[i] >= 0 ? __ldcg(&p.owner[s[i]]) : 0;  // atomics work in L2
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (s[i] < 0) continue;
+                if (o[i] != r0 + i * kPlanThreads) {
+                    p.live[r0 + i * kPlanThreads] = -1;
+                    atomicOr(&sm.flags, kPlanSlotTwice);
+                } else if (a.busy) {
+                    a.busy[s[i]] = 1;
+                }
             }
         }
         __syncthreads();
-        if (all.tokens > 0) {
+        if (carry.fresh > 0) {
             // the lowest free slots, in order, as far as they are needed
             unsigned found = 0;
-            for (int s0 = 0; s0 < p.slots && found < all.tokens; s0 += 16 * kPlanThreads) {
+            for (int s0 = 0; s0 < p.slots && found < carry.fresh; s0 += 16 * kPlanThreads) {
                 const int b0 = s0 + 16 * tid;
-                unsigned free = 0;
-                for (int i = 0; i < 16; i++)
-                    if (b0 + i < p.slots && a.busy[b0 + i] == 0) free |= 1u << i;
-                Pair sum;
-                unsigned k = found + block_scan({(unsigned)__popc(free), 0}, sm, &sum).tokens;
-                for (; free && k < all.tokens; free &= free - 1) p.list[k++] = b0 + __ffs(free) - 1;
-                found += sum.tokens;
+                unsigned free = b0 < p.slots ? zero_bytes(a.busy, b0, p.slots) : 0;
+                Sums sum;
+                unsigned k = found + block_scan({0, 0, (unsigned)__popc(free)}, sm, &sum).fresh;
+                for (; free && k < carry.fresh; free &= free - 1) p.list[k++] = b0 + __ffs(free) - 1;
+                found += sum.fresh;
             }
             __syncthreads();
-            unsigned k = rank.tokens;
-            for (int r = r0; r < r1; r++) {
-                if (p.slot[r] != -2) continue;
-                if (k < found) {
-                    const int s = p.list[k];
-                    p.slot[r] = s;
-                    p.live[r] = s;
-                    a.busy[s] = 1;
-                } else {
-                    p.slot[r] = -1;
-                    p.live[r] = -1;
-                    atomicOr(flags, kPlanNoSlot);
+            for (int r0 = tid; r0 < a.n; r0 += 4 * kPlanThreads) {
+                int s[4], got[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) s[i] = r0 + i * kPlanThreads < a.n ? p.slot[r0 + i * kPlanThreads] : -1;
+#pragma unroll
+                for (int i = 0; i < 4; i++) got[i] = s[i] <= -2 && (unsigned)(-2 - s[i]) < found ? p.list[-2 - s[i]] : -1;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (s[i] > -2) continue;
+                    if (got[i] >= 0)
+                        a.busy[got[i]] = 1;
+                    else
+                        atomicOr(&sm.flags, kPlanNoSlot);
+                    p.slot[r0 + i * kPlanThreads] = got[i];
+                    p.live[r0 + i * kPlanThreads] = got[i];
                 }
-                k++;
             }
         }
+        __syncthreads();
     }
-    __syncthreads();
     if (tid == 0) {
-        p.head[0] = *flags;
+        p.head[0] = sm.flags;
         p.head[1] = a.n;
-        p.head[2] = (int)rows_used;
-        p.head[3] = (int)blocks_used;
+        p.head[2] = rows;
+        p.head[3] = blocks;
     }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) k_plan(PlanArgs a, int token_ctas)
 {
-    __shared__ Pair sm[kPlanThreads / 32];
-    __shared__ int smi[kPlanThreads / 32];
-    __shared__ int mark[kPlanRange], from[kPlanRange];
-    __shared__ int flags;
+    __shared__ Shared sm;
     const PlanView &p = a.p;
     const int tid = threadIdx.x;
-    const int per = (a.n + kPlanThreads - 1) / kPlanThreads;
-    const int r0 = min(a.n, tid * per), r1 = min(a.n, r0 + per);
-    Pair mine = {0, 0}, all;
-    for (int r = r0; r < r1; r++) {
-        const unsigned len = length_of(a, r);
-        mine = add(mine, {len, blocks_of(len)});
-    }
-    Pair at = block_scan(mine, sm, &all);
     if (blockIdx.x == 0) {
-        resolve(a, r0, r1, at, sm, &flags);
+        resolve(a, sm);
         return;
     }
     const int c = blockIdx.x - 1;
     const bool tokens = c < token_ctas;
     const unsigned x0 = (unsigned)(tokens ? c : c - token_ctas) * kPlanRange;
     const unsigned x1 = min(x0 + kPlanRange, (unsigned)(tokens ? p.tokens : p.blocks));
-    for (int i = tid; i < kPlanRange; i += kPlanThreads) mark[i] = -1;
+    for (int i = tid; i < kPlanRange; i += kPlanThreads) sm.mark[i] = -1;
+    if (tid == 0) sm.rows = 0;
     __syncthreads();
-    // mark[x] = request whose entries begin at x0 + x (or before, for x = 0);
-    // from[x] = where they begin
-    for (int r = r0; r < r1; r++) {
-        const unsigned len = length_of(a, r);
-        const Pair end = add(at, {len, blocks_of(len)});
-        if (end.tokens > (unsigned)p.tokens) break;  // this request and all after it have no tokens
-        const unsigned lo = tokens ? at.tokens : at.blocks, hi = tokens ? end.tokens : end.blocks;
-        if (lo < hi && lo < x1 && hi > x0) {
-            const int x = lo > x0 ? (int)(lo - x0) : 0;
-            mark[x] = r;
-            from[x] = (int)lo;
+    // mark[x]: the request whose entries begin at x0 + x (or before, for x = 0);
+    // from[x]: where they begin
+    Sums carry = {0, 0, 0};
+    for (int r0 = 0; r0 < a.n; r0 += kPlanRange) {
+        const int r = r0 + kPer * tid;
+        int n[kPer];
+        four(a.lengths, r, a.n, n);
+        Sums mine = {0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kPer; i++) mine = add(mine, {length_of(n[i]), blocks_of(length_of(n[i])), 0});
+        Sums all, at = add(carry, block_scan(mine, sm, &all));
+        carry = add(carry, all);
+        unsigned end = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; i++) {
+            const unsigned len = length_of(n[i]), lo = tokens ? at.tokens : at.blocks;
+            at = add(at, {len, blocks_of(len), 0});
+            if (at.tokens > (unsigned)p.tokens) break;  // this request and all after it have no tokens
+            const unsigned hi = tokens ? at.tokens : at.blocks;
+            end = hi;
+            if (lo < hi && lo < x1 && hi > x0) {
+                const int x = lo > x0 ? (int)(lo - x0) : 0;
+                sm.mark[x] = r + i;
+                sm.from[x] = (int)lo;
+            }
         }
-        at = end;
+        if (end > x0) atomicMax(&sm.rows, end);  // how far the batch reaches
+        if ((tokens ? carry.tokens : carry.blocks) >= x1 || carry.tokens > (unsigned)p.tokens) break;
     }
     __syncthreads();
     int last[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; i++) last[i] = mark[kPer * tid + i] >= 0 ? kPer * tid + i : -1;
-    scan_max(last, smi);
-    // the rows used: beyond them the last request's mark does not count
-    __shared__ unsigned end_of_batch;
-    if (tid == 0) end_of_batch = 0;
-    __syncthreads();
-    // at: the end of this thread's last request, or of the last that fits
-    if (at.tokens <= (unsigned)p.tokens) atomicMax(&end_of_batch, tokens ? at.tokens : at.blocks);
-    __syncthreads();
+    for (int i = 0; i < kPer; i++) last[i] = sm.mark[kPer * tid + i] >= 0 ? kPer * tid + i : -1;
+    scan_max(last, sm.maxima);
+    const unsigned reach = sm.rows;
+    int r_of[kPer], v_of[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; i++) {
         const unsigned x = x0 + kPer * tid + i;
-        if (x >= x1) continue;
-        int r = -1, v = -1;
-        if (last[i] >= 0 && x < end_of_batch) {
-            r = mark[last[i]];
-            v = (int)x - from[last[i]];
-            v = tokens ? v + (a.contexts ? a.contexts[r] : 0) : v * kBlockTokens;
+        r_of[i] = v_of[i] = -1;
+        if (last[i] >= 0 && x < reach) {
+            const int r = sm.mark[last[i]], v = (int)x - sm.from[last[i]];
+            r_of[i] = r;
+            v_of[i] = tokens ? v + (a.contexts ? a.contexts[r] : 0) : v * kBlockTokens;
         }
-        (tokens ? p.token_request : p.block_request)[x] = r;
-        (tokens ? p.token_position : p.block_first)[x] = v;
+    }
+    int *of = tokens ? p.token_request : p.block_request, *first = tokens ? p.token_position : p.block_first;
+    const unsigned x = x0 + kPer * tid;
+    static_assert(kPer == 4, "an entry group is one 16-byte vector");
+    if (x + kPer <= x1) {
+        *reinterpret_cast<int4 *>(of + x) = make_int4(r_of[0], r_of[1], r_of[2], r_of[3]);
+        *reinterpret_cast<int4 *>(first + x) = make_int4(v_of[0], v_of[1], v_of[2], v_of[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (x + i < x1) {
+                of[x + i] = r_of[i];
+                first[x + i] = v_of[i];
+            }
     }
 }
 
