@@ -3,7 +3,7 @@
 // One launch.  Every CTA scans all lengths for itself (at most 65536 of them,
 // from L2) instead of waiting for a scan kernel: the plan is latency-bound, and
 // a second launch would cost more than the repeated scan.  The first CTA
-// resolves the slots; the others each write 2048 entries of the token map or of
+// resolves the slots; the others each write 4096 entries of the token map or of
 // the block table, which is a search for the request that covers an entry: the
 // requests that begin in the CTA's range mark their first entry, and a running
 // maximum over the marks finds the last request at or before each entry.
@@ -12,8 +12,8 @@
 namespace stepq {
 namespace {
 
-constexpr int kPlanThreads = 512;
-constexpr int kPlanRange = 2048;  // entries of a CTA, and requests of a turn
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanRange = 4096;  // entries of a CTA, and requests of a turn
 constexpr int kPer = kPlanRange / kPlanThreads;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr unsigned kSat = 1u << 30;  // sums stop here (the largest token count is 2^28)
@@ -87,11 +87,27 @@ __device__ void scan_max(int *v, int *sm)
     for (int i = 0; i < kPer; i++) v[i] = max(v[i], before);
 }
 
-// Four consecutive lengths (0 past the batch).
+// Four consecutive entries from r on (a multiple of 4) of n: as one vector where
+// that is aligned.  0 past the end; nothing is written there.
 __device__ __forceinline__ void four(const int *p, int r, int n, int *x)
 {
+    if (r + kPer <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const int4 v = *reinterpret_cast<const int4 *>(p + r);
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
 #pragma unroll
-    for (int i = 0; i < kPer; i++) x[i] = r + i < n ? p[r + i] : 0;
+        for (int i = 0; i < kPer; i++) x[i] = r + i < n ? p[r + i] : 0;
+    }
+}
+__device__ __forceinline__ void put_four(int *p, int r, int n, const int *x)  // p aligned: an array of the plan
+{
+    if (r + kPer <= n) {
+        *reinterpret_cast<int4 *>(p + r) = make_int4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; i++)
+            if (r + i < n) p[r + i] = x[i];
+    }
 }
 
 // Which of 16 bytes from `at` on are zero, as bits.
@@ -118,7 +134,6 @@ __device__ void resolve(const PlanArgs &a, Shared &sm)
     if (tid == 0) {
         sm.flags = 0;
         sm.rows = sm.blocks = 0;
-        p.starts[0] = p.block_starts[0] = 0;
     }
     __syncthreads();
     Sums carry = {0, 0, 0};
@@ -142,16 +157,17 @@ __device__ void resolve(const PlanArgs &a, Shared &sm)
         Sums all, at = add(carry, block_scan(mine, sm, &all));
         carry = add(carry, all);
         unsigned rows = 0, blocks = 0;
-        int bad = 0;
+        int bad = 0, start[kPer], bstart[kPer], live[kPer], fresh[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; i++) {
-            if (r + i >= a.n) continue;
-            const unsigned before = at.fresh;
-            at = add(at, {len[i], blocks_of(len[i]), (unsigned)ask[i]});
             // a request whose tokens pass the capacity ends the batch: it and all after it have none
+            start[i] = at.tokens <= (unsigned)p.tokens ? (int)at.tokens : -1;  // -1: set to the last end below
+            bstart[i] = (int)at.blocks;
+            const unsigned rank = at.fresh;
+            at = add(at, {len[i], blocks_of(len[i]), (unsigned)ask[i]});
+            live[i] = fresh[i] = 0;
+            if (r + i >= a.n) continue;
             const bool fits = at.tokens <= (unsigned)p.tokens;
-            p.starts[r + i + 1] = fits ? (int)at.tokens : -1;  // -1: set to the last end below
-            p.block_starts[r + i + 1] = (int)at.blocks;
             if (fits) {
                 rows = at.tokens;
                 blocks = at.blocks;
@@ -167,18 +183,23 @@ __device__ void resolve(const PlanArgs &a, Shared &sm)
             int s = slot[i];
             if (s < 0 || s >= p.slots) {
                 if (take && ask[i]) {
-                    s = -2 - (int)before;  // gets the free slot of this rank below
+                    s = -2 - (int)rank;  // gets the free slot of this rank below
                 } else {
                     if (take) bad |= kPlanBadSlot;
                     take = false;
                     s = -1;
                 }
             }
-            p.slot[r + i] = s;
-            p.live[r + i] = take && s >= 0 ? s : -1;
-            p.fresh[r + i] = ctx[i] == 0;
+            slot[i] = s;
+            live[i] = take && s >= 0 ? s : -1;
+            fresh[i] = ctx[i] == 0;
             if (take && s >= 0 && a.slots) p.owner[s] = 0x7fffffff;
         }
+        put_four(p.starts, r, a.n, start);
+        put_four(p.block_starts, r, a.n, bstart);
+        put_four(p.slot, r, a.n, slot);
+        put_four(p.live, r, a.n, live);
+        put_four(p.fresh, r, a.n, fresh);
         if (rows) atomicMax(&sm.rows, rows);
         if (blocks) atomicMax(&sm.blocks, blocks);
         if (bad) atomicOr(&sm.flags, bad);
@@ -187,13 +208,14 @@ __device__ void resolve(const PlanArgs &a, Shared &sm)
     const int rows = (int)sm.rows, blocks = (int)sm.blocks;
     if (sm.flags & kPlanTooMany)
         for (int r = tid; r < a.n; r += kPlanThreads)
-            if (p.starts[r + 1] < 0) {
-                p.starts[r + 1] = rows;
-                p.block_starts[r + 1] = blocks;
+            if (p.starts[r] < 0) {
+                p.starts[r] = rows;
+                p.block_starts[r] = blocks;
             }
-    for (int r = a.n + tid; r < p.requests; r += kPlanThreads) {
-        p.starts[r + 1] = rows;
-        p.block_starts[r + 1] = blocks;
+    for (int r = a.n + tid; r <= p.requests; r += kPlanThreads) {
+        p.starts[r] = rows;
+        p.block_starts[r] = blocks;
+        if (r == p.requests) break;
         p.slot[r] = -1;
         p.live[r] = -1;
         p.fresh[r] = 0;
