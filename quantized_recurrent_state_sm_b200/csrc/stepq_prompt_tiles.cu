@@ -13,10 +13,10 @@ namespace stepq {
 namespace {
 
 using dev::ldsm4;
+using dev::ldsm4_t;
 using dev::mma16816;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kLd = kC + 4;  // row of a [64][64] fp32 matrix in shared memory
 
 // Four consecutive elements.
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
@@ -40,12 +40,11 @@ __device__ __forceinline__ float warp_max(float4 x)
     return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(m)));
 }
 
-// One row of an operand (4 elements a lane) as scaled halves into the tile's
-// image in the scratch, and into the tile in shared memory if there is one;
-// returns the row's unscale.  NP: halves kept.  EXACT: binary16 inputs are
-// their own halves.
+// One row of an operand (4 elements a lane) as scaled halves into a tile, in
+// shared or global memory; returns the row's unscale.  NP: halves kept.  EXACT:
+// binary16 inputs are their own halves.
 template <int NP, bool EXACT>
-__device__ __forceinline__ float put_row(float4 x, int row, int l, char *tile, char *image)
+__device__ __forceinline__ float put_row(float4 x, int row, int l, char *tile)
 {
     float scale = 1.f, back = 1.f;
     if (!EXACT) dev::row_scale(warp_max(x), &scale, &back);
@@ -53,15 +52,21 @@ __device__ __forceinline__ float put_row(float4 x, int row, int l, char *tile, c
     dev::split_half(x.x * scale, x.y * scale, &hi[0], &lo[0]);
     dev::split_half(x.z * scale, x.w * scale, &hi[1], &lo[1]);
     const int at = tile_at(row, 4 * l);
-    const uint2 h = make_uint2(hi[0], hi[1]), o = make_uint2(lo[0], lo[1]);
-    *reinterpret_cast<uint2 *>(image + at) = h;
-    if (tile) *reinterpret_cast<uint2 *>(tile + at) = h;
-    if (NP == 2) {
-        *reinterpret_cast<uint2 *>(image + kTileBytes + at) = o;
-        if (tile) *reinterpret_cast<uint2 *>(tile + kTileBytes + at) = o;
-    }
+    *reinterpret_cast<uint2 *>(tile + at) = make_uint2(hi[0], hi[1]);
+    if (NP == 2) *reinterpret_cast<uint2 *>(tile + kTileBytes + at) = make_uint2(lo[0], lo[1]);
     return back;
 }
+
+// Bulk copies from shared memory to the scratch, by one thread; the shared
+// memory may be written again after the wait.
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(dev::smem_addr(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // acc[j] = rows 16 m .. 16 m + 15 of A times rows 8 j .. of B transposed, for
 // the column tiles j < tiles (a multiple of 2): A and B operand tiles in
@@ -101,154 +106,261 @@ __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, con
     }
 }
 
-// ---- [64][64] lower-triangular fp32 matrices in shared memory --------------
+// ---- the inverse and the squares ---------------------------------------------
+//
+// A (strictly lower triangular, [64][64]) and P are held as accumulators: warp m
+// of 0-3 has rows 16 m .. of A, warp 4 + m those of P, all columns.  With T = (I +
+// A)^-1 in blocks of 16: T_mm by substitution, then row by row
+//   T_m = T_mm - (T_mm A_m) T_(<m),
+// products on the tensor cores; P T likewise.  A left operand comes from the
+// accumulators of its own warp, a right one from halves in shared memory, whose
+// row scales (inner indices of the product) are multiplied into the left one.
 
-// acc += x . the rows m .. m + 3 of Y at four columns.
-__device__ __forceinline__ void fma4(float4 &acc, float4 x, const float *Y)
-{
-    const float4 y0 = *reinterpret_cast<const float4 *>(Y), y1 = *reinterpret_cast<const float4 *>(Y + kLd),
-                 y2 = *reinterpret_cast<const float4 *>(Y + 2 * kLd), y3 = *reinterpret_cast<const float4 *>(Y + 3 * kLd);
-    acc.x = fmaf(x.x, y0.x, fmaf(x.y, y1.x, fmaf(x.z, y2.x, fmaf(x.w, y3.x, acc.x))));
-    acc.y = fmaf(x.x, y0.y, fmaf(x.y, y1.y, fmaf(x.z, y2.y, fmaf(x.w, y3.y, acc.y))));
-    acc.z = fmaf(x.x, y0.z, fmaf(x.y, y1.z, fmaf(x.z, y2.z, fmaf(x.w, y3.z, acc.z))));
-    acc.w = fmaf(x.x, y0.w, fmaf(x.y, y1.w, fmaf(x.z, y2.w, fmaf(x.w, y3.w, acc.w))));
-}
+constexpr int kDiagLd = 20;
+struct Squares {
+    __align__(128) char a[kSquareBytes], t[kSquareBytes], p[kSquareBytes];  // halves of A, T and P T
+    float diag[4][16][kDiagLd], tdiag[4][16][kDiagLd];  // the diagonal blocks of A and T
+    float a_back[kC], t_back[kC], p_back[kC];           // unscales of the rows
+};
 
-// inv_21 = -inv_22 A_21 inv_11 for the pairs of H x H diagonal blocks; tmp: room
-// for another matrix.
-template <int H>
-__device__ __forceinline__ void invert_step(const float *A, float *inv, float *tmp)
+__device__ __forceinline__ float quad_max(float m)
 {
-    const int tid = threadIdx.x;
-    constexpr int tasks = kC / (2 * H) * H * H / 4;  // four columns of a row each: at most 256
-    const int pair = tid / (H * H / 4), i = tid / (H / 4) % H, j = tid % (H / 4) * 4;
-    const int lo = 2 * H * pair, hi = lo + H;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tid < tasks) {
-#pragma unroll
-        for (int m = 0; m < H; m += 4) fma4(x, *reinterpret_cast<const float4 *>(A + (hi + i) * kLd + lo + m), inv + (lo + m) * kLd + lo + j);
-        *reinterpret_cast<float4 *>(tmp + (hi + i) * kLd + lo + j) = x;
-    }
-    __syncthreads();
-    if (tid < tasks) {
-        x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int m = 0; m < H; m += 4) fma4(x, *reinterpret_cast<const float4 *>(inv + (hi + i) * kLd + hi + m), tmp + (hi + m) * kLd + lo + j);
-        *reinterpret_cast<float4 *>(inv + (hi + i) * kLd + lo + j) = make_float4(-x.x, -x.y, -x.z, -x.w);
-    }
-    __syncthreads();
-}
-
-// inv = (I + A)^-1 for the strictly lower triangular A: the four diagonal blocks
-// of 16 by substitution, a column a thread, then the blocks below in two steps.
-// Blocks above the diagonal stay as they are, except 16 x 32 ones inside a
-// diagonal block of 32, which are set to zero (they are read as such).
-__device__ __forceinline__ void invert_lower(const float *A, float *inv, float *tmp)
-{
-    const int tid = threadIdx.x;
-    if (tid < kC) {
-        const int b = tid & ~15, j = tid & 15;
-        float x[16];
-#pragma unroll
-        for (int r = 0; r < 16; r++) {
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int m = 0; m < r; m += 4) {
-                const float4 y = *reinterpret_cast<const float4 *>(A + (b + r) * kLd + b + m);
-                s0 = fmaf(y.x, x[m], s0);
-                if (m + 1 < r) s1 = fmaf(y.y, x[m + 1], s1);
-                if (m + 2 < r) s0 = fmaf(y.z, x[m + 2], s0);
-                if (m + 3 < r) s1 = fmaf(y.w, x[m + 3], s1);
-            }
-            x[r] = r < j ? 0.f : (r == j ? 1.f : -(s0 + s1));
-            inv[(b + r) * kLd + b + j] = x[r];
-        }
-    } else if (tid < 2 * kC) {
-        // the upper 16 x 16 blocks of the two diagonal blocks of 32
-        const int b = (tid - kC) >> 5, i = (tid - kC) & 15, e = (tid - kC) >> 4 & 1;
-#pragma unroll
-        for (int j = 0; j < 8; j += 4) *reinterpret_cast<float4 *>(inv + (32 * b + i) * kLd + 32 * b + 16 + 8 * e + j) = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    __syncthreads();
-    invert_step<16>(A, inv, tmp);
-    invert_step<32>(A, inv, tmp);
-}
-
-// out = X Y for lower-triangular X and Y, two rows and four columns a thread and
-// turn; the blocks of 16 x 16 on and below the diagonal are written (those of X
-// and Y hold zeros above the diagonal).
-__device__ __forceinline__ void lower_product(const float *X, const float *Y, float *out)
-{
-    for (int x = threadIdx.x; x < kC / 2 * (kC / 4); x += blockDim.x) {
-        const int i = x / (kC / 4) * 2, j = x % (kC / 4) * 4;
-        if ((j & ~15) > i) continue;
-        float4 a0 = make_float4(0.f, 0.f, 0.f, 0.f), a1 = a0;
-        const int last = i | 3;
-        for (int m = j; m <= last; m += 4) {
-            const float4 x0 = *reinterpret_cast<const float4 *>(X + i * kLd + m), x1 = *reinterpret_cast<const float4 *>(X + (i + 1) * kLd + m);
-            fma4(a0, x0, Y + m * kLd + j);
-            fma4(a1, x1, Y + m * kLd + j);
-        }
-        *reinterpret_cast<float4 *>(out + i * kLd + j) = a0;
-        *reinterpret_cast<float4 *>(out + (i + 1) * kLd + j) = a1;
-    }
-}
-
-// The lower triangle of a matrix, rows as scaled halves, into the scratch (256
-// threads, numbered x); the rows' unscales into back[].  Columns past the row's
-// block of 16 are not written (and not read).
-__device__ __forceinline__ void put_square(int x, const float *sq, char *image, float *back)
-{
-    const int row = x >> 2, part = x & 3;  // 16 columns each
-    const bool inside = part <= row >> 4;
-    float v[16], m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (inside) y = *reinterpret_cast<const float4 *>(sq + row * kLd + 16 * part + i);
-        v[i] = y.x; v[i + 1] = y.y; v[i + 2] = y.z; v[i + 3] = y.w;
-        m = fmaxf(fmaxf(fmaxf(m, fabsf(y.x)), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w)));
-    }
     m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-    float scale, b;
-    dev::row_scale(m, &scale, &b);
-    if (part == 0) back[row] = b;
-    if (!inside) return;
-    uint32_t hi[8], lo[8];
+    return fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+}
+
+// Scales of rows g and g + 8 of an accumulator of which `tiles` column tiles count.
+template <int N>
+__device__ __forceinline__ void row_scales(const float (*x)[4], int tiles, float *scale, float *back)
+{
+    float m0 = 0.f, m1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; i++) dev::split_half(v[2 * i] * scale, v[2 * i + 1] * scale, &hi[i], &lo[i]);
+    for (int j = 0; j < N; j++)
+        if (j < tiles) {
+            m0 = fmaxf(m0, fmaxf(fabsf(x[j][0]), fabsf(x[j][1])));
+            m1 = fmaxf(m1, fmaxf(fabsf(x[j][2]), fabsf(x[j][3])));
+        }
+    dev::row_scale(quad_max(m0), &scale[0], &back[0]);
+    dev::row_scale(quad_max(m1), &scale[1], &back[1]);
+}
+
+// `tiles` column tiles of an accumulator as halves into a square's rows 16 m ..
+template <int N>
+__device__ __forceinline__ void put_tiles(const float (*x)[4], int tiles, const float *scale, char *square, int m)
+{
+    const int l = threadIdx.x & 31, g = l >> 2, c = l & 3;
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
-        const int at = square_at(row, 16 * part + 8 * e);
-        *reinterpret_cast<uint4 *>(image + at) = make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-        *reinterpret_cast<uint4 *>(image + kSquareBytes / 2 + at) = make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+    for (int j = 0; j < N; j++)
+        if (j < tiles)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                uint32_t hi, lo;
+                dev::split_half(x[j][2 * e] * scale[e], x[j][2 * e + 1] * scale[e], &hi, &lo);
+                char *at = square + square_at(16 * m + g + 8 * e, 8 * j + 2 * c);
+                *reinterpret_cast<uint32_t *>(at) = hi;
+                *reinterpret_cast<uint32_t *>(at + kSquareBytes / 2) = lo;
+            }
+}
+
+// out += x y: x an accumulator of `blocks` blocks of 16 columns (scaled), y the
+// rows of a lower-triangular square's blocks, out their column tiles.
+template <int N>
+__device__ __forceinline__ void times_square(float (*out)[4], const float (*x)[4], int blocks, const float *scale, const char *square, int first_row, bool lower)
+{
+    const int l = threadIdx.x & 31;
+    const uint32_t y0 = dev::smem_addr(square);
+#pragma unroll
+    for (int i = 0; i < N / 2; i++) {
+        if (i >= blocks) continue;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            dev::split_half(x[2 * i + e][0] * scale[0], x[2 * i + e][1] * scale[0], &hi[2 * e], &lo[2 * e]);
+            dev::split_half(x[2 * i + e][2] * scale[1], x[2 * i + e][3] * scale[1], &hi[2 * e + 1], &lo[2 * e + 1]);
+        }
+        const int tiles = lower ? 2 * i + 2 : N;
+        uint32_t b[N][2], d[N][2];
+#pragma unroll
+        for (int j = 0; j < N; j += 2)
+            if (j < tiles) {
+                const uint32_t at = y0 + square_at(first_row + 16 * i + (l & 15), 8 * j + (l >> 4) * 8);
+                ldsm4_t(b[j], b[j + 1], at);
+                ldsm4_t(d[j], d[j + 1], at + kSquareBytes / 2);
+            }
+#pragma unroll
+        for (int j = 0; j < N; j++)
+            if (j < tiles) mma16816(out[j], lo[0], lo[1], lo[2], lo[3], b[j][0], b[j][1]);
+#pragma unroll
+        for (int j = 0; j < N; j++)
+            if (j < tiles) mma16816(out[j], hi[0], hi[1], hi[2], hi[3], d[j][0], d[j][1]);
+#pragma unroll
+        for (int j = 0; j < N; j++)
+            if (j < tiles) mma16816(out[j], hi[0], hi[1], hi[2], hi[3], b[j][0], b[j][1]);
     }
 }
 
-// From A (strictly lower triangular) and P to the squares of the scratch:
-// (I + A)^-1 and P (I + A)^-1 (without an A, P itself).  I, tmp: room for two
-// matrices.  Begins and ends with a barrier.
+// From A and P (the accumulators of warps 0-7, zero above the diagonal) to the
+// halves of T and P T in sq.  Warps past the eighth only meet the barriers.
+// Begins with the accumulators written, ends with a barrier.
 template <bool DELTA>
-__device__ __forceinline__ void finish(float *A, float *P, float *I, float *tmp, char *inv_image, char *p_image, float *s_inv, float *s_p)
+__device__ __forceinline__ void finish(float (*acc)[4], Squares &sq)
 {
-    const int x = threadIdx.x;
-    __syncthreads();
-    const float *out = P;
-    if (DELTA) {
-        invert_lower(A, I, tmp);
-        lower_product(P, I, tmp);
-        out = tmp;
+    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3, m = w & 3;
+    float scale[2], back[2];
+    if constexpr (DELTA) {
+        if (w < 4) {
+            row_scales<6>(acc, 2 * m, scale, back);
+            put_tiles<6>(acc, 2 * m, scale, sq.a, m);
+            if (c == 0) {
+                sq.a_back[16 * m + g] = back[0];
+                sq.a_back[16 * m + g + 8] = back[1];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j += 2)
+                if (j == 2 * m)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        *reinterpret_cast<float2 *>(&sq.diag[m][g][8 * e + 2 * c]) = make_float2(acc[j + e][0], acc[j + e][1]);
+                        *reinterpret_cast<float2 *>(&sq.diag[m][g + 8][8 * e + 2 * c]) = make_float2(acc[j + e][2], acc[j + e][3]);
+                    }
+        }
         __syncthreads();
+        if (tid < kC) {  // T_mm, a column a thread
+            const int b = tid >> 4, j = tid & 15;
+            float x[16];
+#pragma unroll
+            for (int r = 0; r < 16; r++) {
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < r; i += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&sq.diag[b][r][i]);
+                    s0 = fmaf(y.x, x[i], s0);
+                    if (i + 1 < r) s1 = fmaf(y.y, x[i + 1], s1);
+                    if (i + 2 < r) s0 = fmaf(y.z, x[i + 2], s0);
+                    if (i + 3 < r) s1 = fmaf(y.w, x[i + 3], s1);
+                }
+                x[r] = r < j ? 0.f : (r == j ? 1.f : -(s0 + s1));
+                sq.tdiag[b][r][j] = x[r];
+            }
+        }
+        __syncthreads();
+        float td[2][4];  // T_mm as an accumulator of two column tiles
+        if (w < 4) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float2 x = *reinterpret_cast<const float2 *>(&sq.tdiag[m][g][8 * e + 2 * c]), y = *reinterpret_cast<const float2 *>(&sq.tdiag[m][g + 8][8 * e + 2 * c]);
+                td[e][0] = x.x; td[e][1] = x.y; td[e][2] = y.x; td[e][3] = y.y;
+            }
+            if (m == 0) {
+                row_scales<2>(td, 2, scale, back);
+                put_tiles<2>(td, 2, scale, sq.t, 0);
+                if (c == 0) {
+                    sq.t_back[g] = back[0];
+                    sq.t_back[g + 8] = back[1];
+                }
+            } else {
+                float x[2][4];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const float2 f = *reinterpret_cast<const float2 *>(&sq.a_back[16 * m + 8 * e + 2 * c]);
+                    x[e][0] = td[e][0] * f.x; x[e][1] = td[e][1] * f.y; x[e][2] = td[e][2] * f.x; x[e][3] = td[e][3] * f.y;
+                }
+                row_scales<2>(x, 2, scale, back);
+                // T_mm A_m takes A_m's place (the products of one block of 16 rows of A)
+                float y[6][4] = {};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    dev::split_half(x[e][0] * scale[0], x[e][1] * scale[0], &hi[2 * e], &lo[2 * e]);
+                    dev::split_half(x[e][2] * scale[1], x[e][3] * scale[1], &hi[2 * e + 1], &lo[2 * e + 1]);
+                }
+                const uint32_t y0 = dev::smem_addr(sq.a);
+#pragma unroll
+                for (int j = 0; j < 6; j += 2) {
+                    if (j >= 2 * m) continue;
+                    uint32_t b[2][2], d[2][2];
+                    const uint32_t at = y0 + square_at(16 * m + (l & 15), 8 * j + (l >> 4) * 8);
+                    ldsm4_t(b[0], b[1], at);
+                    ldsm4_t(d[0], d[1], at + kSquareBytes / 2);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) mma16816(y[j + e], lo[0], lo[1], lo[2], lo[3], b[e][0], b[e][1]);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) mma16816(y[j + e], hi[0], hi[1], hi[2], hi[3], d[e][0], d[e][1]);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) mma16816(y[j + e], hi[0], hi[1], hi[2], hi[3], b[e][0], b[e][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < 6; j++) {
+                    acc[j][0] = y[j][0] * back[0]; acc[j][1] = y[j][1] * back[0];
+                    acc[j][2] = y[j][2] * back[1]; acc[j][3] = y[j][3] * back[1];
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int mm = 1; mm < 4; mm++) {
+            if (w == mm) {
+#pragma unroll
+                for (int j = 0; j < 6; j++) {
+                    if (j >= 2 * mm) continue;
+                    const float2 f = *reinterpret_cast<const float2 *>(&sq.t_back[8 * j + 2 * c]);
+                    acc[j][0] *= f.x; acc[j][1] *= f.y; acc[j][2] *= f.x; acc[j][3] *= f.y;
+                }
+                row_scales<6>(acc, 2 * mm, scale, back);
+                float t[8][4] = {};
+                times_square<6>(t, acc, mm, scale, sq.t, 0, true);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    t[j][0] *= -back[0]; t[j][1] *= -back[0]; t[j][2] *= -back[1]; t[j][3] *= -back[1];
+                    if ((j & ~1) == 2 * mm)
+#pragma unroll
+                        for (int e = 0; e < 4; e++) t[j][e] = td[j & 1][e];
+                }
+                row_scales<8>(t, 2 * mm + 2, scale, back);
+                put_tiles<8>(t, 2 * mm + 2, scale, sq.t, mm);
+                if (c == 0) {
+                    sq.t_back[16 * mm + g] = back[0];
+                    sq.t_back[16 * mm + g + 8] = back[1];
+                }
+            }
+            __syncthreads();
+        }
     }
-    if (x < 256) put_square(x, out, p_image, s_p);
-    if (DELTA) {  // by the other half of the threads, where there are that many
-        if (blockDim.x == 256)
-            put_square(x, I, inv_image, s_inv);
-        else if (x >= 256)
-            put_square(x - 256, I, inv_image, s_inv);
+    if (w >= 4 && w < 8) {
+        float o[8][4] = {};
+        if constexpr (DELTA) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                if (j >= 2 * m + 2) continue;
+                const float2 f = *reinterpret_cast<const float2 *>(&sq.t_back[8 * j + 2 * c]);
+                acc[j][0] *= f.x; acc[j][1] *= f.y; acc[j][2] *= f.x; acc[j][3] *= f.y;
+            }
+            row_scales<8>(acc, 2 * m + 2, scale, back);
+            times_square<8>(o, acc, m + 1, scale, sq.t, 0, true);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                o[j][0] *= back[0]; o[j][1] *= back[0]; o[j][2] *= back[1]; o[j][3] *= back[1];
+            }
+        }
+        const float(*out)[4] = DELTA ? o : acc;
+        row_scales<8>(out, 2 * m + 2, scale, back);
+        put_tiles<8>(out, 2 * m + 2, scale, sq.p, m);
+        if (c == 0) {
+            sq.p_back[16 * m + g] = back[0];
+            sq.p_back[16 * m + g + 8] = back[1];
+        }
     }
+    fence_async();
     __syncthreads();
+}
+
+// The halves into the scratch (one thread; they may be written again after bulk_wait_read).
+template <bool DELTA>
+__device__ __forceinline__ void put_squares(const Squares &sq, uint8_t *inv_image, uint8_t *p_image)
+{
+    if (DELTA) bulk_s2g(inv_image, sq.t, kSquareBytes);
+    bulk_s2g(p_image, sq.p, kSquareBytes);
+    bulk_commit();
 }
 
 // What a CTA works on: a block of a live request.
@@ -278,7 +390,7 @@ template <class T, int V, int NP>
 __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_block, Scratch sc)
 {
     extern __shared__ __align__(128) char smem[];
-    __shared__ float ek[kC], eq[kC], s_beta[kC], s_pre[kC], s_suf[kC], s_inv[kC], s_p[kC], s_blk[4], s_diag[4][16][17];
+    __shared__ float ek[kC], eq[kC], s_beta[kC], s_pre[kC], s_suf[kC], s_blk[4], s_diag[4][16][17];
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
     const int heads_k = a.heads / a.share;
     Block k;
@@ -295,8 +407,6 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
     }
     char *tk = smem, *tq = smem + NP * kTileBytes;
     {
-        const size_t at = ((size_t)k.b * heads_k + hq) * NP * kTileBytes;
-        char *ik = reinterpret_cast<char *>(a.scratch) + sc.k + at, *iq = reinterpret_cast<char *>(a.scratch) + sc.q + at;
         const T *kg = static_cast<const T *>(a.k) + hq * kDK, *qg = static_cast<const T *>(a.q) + hq * kDK;
         constexpr bool exact = std::is_same<T, __half>::value;
         float4 xk[kC / 8], xq[kC / 8];
@@ -312,30 +422,38 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
 #pragma unroll
         for (int i = 0; i < kC / 8; i++) {
             const int row = 8 * w + i;
-            const float bk = put_row<NP, exact>(xk[i], row, l, tk, ik), bq = put_row<NP, exact>(xq[i], row, l, tq, iq);
+            const float bk = put_row<NP, exact>(xk[i], row, l, tk), bq = put_row<NP, exact>(xq[i], row, l, tq);
             if (l == 0) {
                 ek[row] = bk;
                 eq[row] = bq;
             }
         }
     }
+    fence_async();
     __syncthreads();
+    if (tid == 0) {
+        const size_t at = ((size_t)k.b * heads_k + hq) * NP * kTileBytes;
+        bulk_s2g(a.scratch + sc.k + at, tk, NP * kTileBytes);
+        bulk_s2g(a.scratch + sc.q + at, tq, NP * kTileBytes);
+        bulk_commit();
+    }
     const int m = w & 3;  // rows 16 m + g, + 8
     const bool is_q = w >= 4;
-    float acc[kC / 8][4] = {};
-    if (is_q || V != kLinear) rows_product<NP>(acc, is_q ? tq : tk, tk, m, 2 * m + 2);
+    float raw[kC / 8][4] = {};
+    if (is_q || V != kLinear) rows_product<NP>(raw, is_q ? tq : tk, tk, m, 2 * m + 2);
     {
         const float r0 = (is_q ? eq : ek)[16 * m + g], r1 = (is_q ? eq : ek)[16 * m + g + 8];
 #pragma unroll
         for (int j = 0; j < kC / 8; j++) {
             const float c0 = ek[8 * j + 2 * c], c1 = ek[8 * j + 2 * c + 1];
-            acc[j][0] *= r0 * c0; acc[j][1] *= r0 * c1; acc[j][2] *= r1 * c0; acc[j][3] *= r1 * c1;
+            raw[j][0] *= r0 * c0; raw[j][1] *= r0 * c1; raw[j][2] *= r1 * c0; raw[j][3] *= r1 * c1;
         }
     }
-    // the tiles are done with: their room holds the fp32 matrices
-    float *sA = reinterpret_cast<float *>(smem), *sP = sA + kC * kLd, *sI = sP + kC * kLd, *sX = sI + kC * kLd;
+    // the tiles are done with: their room holds the squares
+    Squares &sq = *reinterpret_cast<Squares *>(smem);
     for (int v = 0; v < a.share; v++) {
         const int h = hq * a.share + v;
+        __syncthreads();  // the vectors of the head before are read
         if (tid < kC) {
             float p = alpha, q = __shfl_down_sync(kFull, alpha, 1, 16);
             if ((l & 15) == 15) q = 1.f;
@@ -362,15 +480,15 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
             alpha = a.alpha[gate0 + v + 1];
             beta = a.beta[gate0 + v + 1];
         }
+        if (tid == 0) bulk_wait_read();  // the tiles, or the squares before, are copied
         __syncthreads();
-        if (is_q || V != kLinear) {
-            float *dst = is_q ? sP : sA;
+        float acc[kC / 8][4];
+        {
             const int i0 = g, i1 = g + 8;  // rows within the block of 16
             const float b0 = is_q ? 1.f : s_beta[16 * m + i0], b1 = is_q ? 1.f : s_beta[16 * m + i1];
             float f0 = s_pre[16 * m + i0] * b0, f1 = s_pre[16 * m + i1] * b1;
 #pragma unroll
             for (int jb = kC / 16 - 1; jb >= 0; jb--) {
-                if (jb > m) continue;
                 if (jb + 1 < m) {  // another 16 tokens between
                     f0 *= s_blk[jb + 1];
                     f1 *= s_blk[jb + 1];
@@ -378,25 +496,25 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const int j = 2 * jb + e, s = 8 * j + 2 * c, si = s & 15;
-                    float2 x, y;
-                    if (jb == m) {
-                        x.x = (is_q ? si <= i0 : si < i0) ? acc[j][0] * s_diag[m][i0][si] * b0 : 0.f;
-                        x.y = (is_q ? si + 1 <= i0 : si + 1 < i0) ? acc[j][1] * s_diag[m][i0][si + 1] * b0 : 0.f;
-                        y.x = (is_q ? si <= i1 : si < i1) ? acc[j][2] * s_diag[m][i1][si] * b1 : 0.f;
-                        y.y = (is_q ? si + 1 <= i1 : si + 1 < i1) ? acc[j][3] * s_diag[m][i1][si + 1] * b1 : 0.f;
+                    float *x = acc[j];
+                    if (jb > m) {
+                        x[0] = x[1] = x[2] = x[3] = 0.f;
+                    } else if (jb == m) {
+                        x[0] = (is_q ? si <= i0 : si < i0) ? raw[j][0] * s_diag[m][i0][si] * b0 : 0.f;
+                        x[1] = (is_q ? si + 1 <= i0 : si + 1 < i0) ? raw[j][1] * s_diag[m][i0][si + 1] * b0 : 0.f;
+                        x[2] = (is_q ? si <= i1 : si < i1) ? raw[j][2] * s_diag[m][i1][si] * b1 : 0.f;
+                        x[3] = (is_q ? si + 1 <= i1 : si + 1 < i1) ? raw[j][3] * s_diag[m][i1][si + 1] * b1 : 0.f;
                     } else {
                         const float2 q = *reinterpret_cast<const float2 *>(&s_suf[s]);
-                        x = make_float2(acc[j][0] * (f0 * q.x), acc[j][1] * (f0 * q.y));
-                        y = make_float2(acc[j][2] * (f1 * q.x), acc[j][3] * (f1 * q.y));
+                        x[0] = raw[j][0] * (f0 * q.x); x[1] = raw[j][1] * (f0 * q.y);
+                        x[2] = raw[j][2] * (f1 * q.x); x[3] = raw[j][3] * (f1 * q.y);
                     }
-                    *reinterpret_cast<float2 *>(dst + (16 * m + i0) * kLd + s) = x;
-                    *reinterpret_cast<float2 *>(dst + (16 * m + i1) * kLd + s) = y;
                 }
             }
         }
         const size_t bh = (size_t)k.b * a.heads + h;
-        finish<V != kLinear>(sA, sP, sI, sX, reinterpret_cast<char *>(a.scratch) + sc.inv + bh * kSquareBytes,
-                             reinterpret_cast<char *>(a.scratch) + sc.p + bh * kSquareBytes, s_inv, s_p);
+        finish<V != kLinear>(acc, sq);
+        if (tid == 0) put_squares<V != kLinear>(sq, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
         if (tid < kC) {
             float *sv = reinterpret_cast<float *>(a.scratch + sc.sv) + bh * kStateFloats;
             float *ov = reinterpret_cast<float *>(a.scratch + sc.ov) + bh * kOutFloats;
@@ -407,13 +525,13 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
             left *= ek[tid];
             sv[tid] = -s_beta[tid] * ct * ek[tid];
             sv[kC + tid] = s_beta[tid];
-            sv[2 * kC + tid] = V == kLinear ? left : s_inv[tid] * left;
+            sv[2 * kC + tid] = V == kLinear ? left : sq.t_back[tid] * left;
             if (tid == kC - 1) sv[3 * kC] = ct;
             ov[tid] = ct * eq[tid];
-            ov[kC + tid] = s_p[tid];
+            ov[kC + tid] = sq.p_back[tid];
         }
-        __syncthreads();
     }
+    if (tid == 0) bulk_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -425,6 +543,7 @@ __global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_blo
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 512;
 constexpr int kRowLd = kDK + 8;  // row of a [64][128] fp32 matrix: fragments of 8 rows x 8 columns fall into different banks
+constexpr int kLd = kC + 8;          // row of a [64][64] fp32 matrix
 constexpr int kGateBytes = (5 * kC * kRowLd + 2 * kC * kLd) * 4;
 
 __device__ __forceinline__ float4 mul4(float4 x, float4 y) { return make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w); }
@@ -433,11 +552,11 @@ template <class T>
 __global__ void __launch_bounds__(kGateThreads) k_gate_tiles(PromptArgs a, int first_block, Scratch sc)
 {
     extern __shared__ __align__(128) char smem[];
-    __shared__ float ek[kC], eq[kC], ek2[kC], s_beta[kC], s_inv[kC], s_p[kC];
+    __shared__ float ek[kC], eq[kC], ek2[kC], s_beta[kC];
     __shared__ float s_ks[kC], s_kb[kC], s_qs[kC], s_qb[kC];  // scale and unscale of the rows of K and Q
     __shared__ __align__(16) float s_blk[4][kDK];
     float *sa = reinterpret_cast<float *>(smem), *sk = sa + kC * kRowLd, *sq = sk + kC * kRowLd, *pre = sq + kC * kRowLd, *suf = pre + kC * kRowLd;
-    float *sA = suf + kC * kRowLd, *sP = sA + kC * kLd, *sI = sk, *sX = sq;  // the last two when K and Q are done with
+    float *sA = suf + kC * kRowLd, *sP = sA + kC * kLd;
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
     Block k;
     const int h = blockIdx.x % a.heads;
@@ -506,8 +625,8 @@ __global__ void __launch_bounds__(kGateThreads) k_gate_tiles(PromptArgs a, int f
             const int row = 4 * w + i, at = row * kRowLd + 4 * l;
             const float4 ct = mul4(before, *reinterpret_cast<const float4 *>(pre + at)), left = mul4(behind, *reinterpret_cast<const float4 *>(suf + at));
             const float4 x = *reinterpret_cast<const float4 *>(sk + at), y = *reinterpret_cast<const float4 *>(sq + at);
-            const float b0 = put_row<2, false>(mul4(x, ct), row, l, nullptr, img + sc.k), b1 = put_row<2, false>(mul4(y, ct), row, l, nullptr, img + sc.q),
-                        b2 = put_row<2, false>(mul4(x, left), row, l, nullptr, img + sc.k2);
+            const float b0 = put_row<2, false>(mul4(x, ct), row, l, img + sc.k), b1 = put_row<2, false>(mul4(y, ct), row, l, img + sc.q),
+                        b2 = put_row<2, false>(mul4(x, left), row, l, img + sc.k2);
             if (l == 0) {
                 ek[row] = b0;
                 eq[row] = b1;
@@ -595,26 +714,39 @@ __global__ void __launch_bounds__(kGateThreads) k_gate_tiles(PromptArgs a, int f
             }
         }
     }
-    finish<true>(sA, sP, sI, sX, reinterpret_cast<char *>(a.scratch) + sc.inv + bh * kSquareBytes,
-                 reinterpret_cast<char *>(a.scratch) + sc.p + bh * kSquareBytes, s_inv, s_p);
+    __syncthreads();
+    // everything but A and P is done with: the squares take its room
+    Squares &squares = *reinterpret_cast<Squares *>(smem);
+    float acc[kC / 8][4] = {};
+    if (w < 8) {
+        const float *src = (w < 4 ? sA : sP) + 16 * (w & 3) * kLd;
+#pragma unroll
+        for (int j = 0; j < kC / 8; j++) {
+            const float2 x = *reinterpret_cast<const float2 *>(src + g * kLd + 8 * j + 2 * c), y = *reinterpret_cast<const float2 *>(src + (g + 8) * kLd + 8 * j + 2 * c);
+            acc[j][0] = x.x; acc[j][1] = x.y; acc[j][2] = y.x; acc[j][3] = y.y;
+        }
+    }
+    finish<true>(acc, squares);
+    if (tid == 0) put_squares<true>(squares, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
     float *sv = reinterpret_cast<float *>(a.scratch + sc.sv) + bh * kStateFloats;
     if (tid < kC) {
         float *ov = reinterpret_cast<float *>(a.scratch + sc.ov) + bh * kOutFloats;
         sv[tid] = -s_beta[tid] * ek[tid];
         sv[kC + tid] = s_beta[tid];
-        sv[2 * kC + tid] = s_inv[tid] * ek2[tid];
+        sv[2 * kC + tid] = squares.t_back[tid] * ek2[tid];
         ov[tid] = eq[tid];
-        ov[kC + tid] = s_p[tid];
+        ov[kC + tid] = squares.p_back[tid];
     } else if (tid >= 128 && tid < 128 + kDK) {
         const int d = tid - 128;
         sv[3 * kC + d] = s_blk[0][d] * s_blk[1][d] * s_blk[2][d] * s_blk[3][d];
     }
+    if (tid == 0) bulk_wait();
 }
 
 template <class T, int V, int NP>
 cudaError_t launch_tiles(const PromptArgs &a, int first, int n, const Scratch &sc, cudaStream_t s)
 {
-    const int dyn = std::max(2 * NP * kTileBytes, 4 * kC * kLd * 4);
+    const int dyn = std::max(2 * NP * kTileBytes, (int)sizeof(Squares));
     cudaError_t e = cudaFuncSetAttribute(k_block_tiles<T, V, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
     if (e != cudaSuccess) return e;
     k_block_tiles<T, V, NP><<<(unsigned)n * (unsigned)(a.heads / a.share), 256, dyn, s>>>(a, first, sc);
