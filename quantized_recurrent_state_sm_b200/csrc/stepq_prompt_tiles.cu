@@ -109,7 +109,7 @@ __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, con
 // ---- the inverse and the squares ---------------------------------------------
 //
 // A (strictly lower triangular, [64][64]) and P are held as accumulators: warp m
-// of 0-3 has rows 16 m .. of A, warp 4 + m those of P, all columns.  With T = (I +
+// of 0-3 has rows 16 m .. of both, all columns.  With T = (I +
 // A)^-1 in blocks of 16: T_mm by substitution, then row by row
 //   T_m = T_mm - (T_mm A_m) T_(<m),
 // products on the tensor cores; P T likewise.  A left operand comes from the
@@ -118,7 +118,7 @@ __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, con
 
 constexpr int kDiagLd = 20;
 struct Squares {
-    __align__(128) char a[kSquareBytes], t[kSquareBytes], p[kSquareBytes];  // halves of A, T and P T
+    __align__(128) char a[kSquareBytes], t[kSquareBytes];  // halves of A, and later of P T; of T
     float diag[4][16][kDiagLd], tdiag[4][16][kDiagLd];  // the diagonal blocks of A and T
     float a_back[kC], t_back[kC], p_back[kC];           // unscales of the rows
 };
@@ -199,11 +199,11 @@ __device__ __forceinline__ void times_square(float (*out)[4], const float (*x)[4
     }
 }
 
-// From A and P (the accumulators of warps 0-7, zero above the diagonal) to the
-// halves of T and P T in sq.  Warps past the eighth only meet the barriers.
-// Begins with the accumulators written, ends with a barrier.
+// From A and P (the accumulators of warps 0-3, zero above the diagonal) to the
+// halves of T and P T in sq.  Warps past the fourth only meet the barriers.
+// Ends with a barrier.
 template <bool DELTA>
-__device__ __forceinline__ void finish(float (*acc)[4], Squares &sq)
+__device__ __forceinline__ void finish(float (*acc)[4], float (*accp)[4], Squares &sq)
 {
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3, m = w & 3;
     float scale[2], back[2];
@@ -326,25 +326,25 @@ __device__ __forceinline__ void finish(float (*acc)[4], Squares &sq)
             __syncthreads();
         }
     }
-    if (w >= 4 && w < 8) {
+    if (w < 4) {
         float o[8][4] = {};
         if constexpr (DELTA) {
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 if (j >= 2 * m + 2) continue;
                 const float2 f = *reinterpret_cast<const float2 *>(&sq.t_back[8 * j + 2 * c]);
-                acc[j][0] *= f.x; acc[j][1] *= f.y; acc[j][2] *= f.x; acc[j][3] *= f.y;
+                accp[j][0] *= f.x; accp[j][1] *= f.y; accp[j][2] *= f.x; accp[j][3] *= f.y;
             }
-            row_scales<8>(acc, 2 * m + 2, scale, back);
-            times_square<8>(o, acc, m + 1, scale, sq.t, 0, true);
+            row_scales<8>(accp, 2 * m + 2, scale, back);
+            times_square<8>(o, accp, m + 1, scale, sq.t, 0, true);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 o[j][0] *= back[0]; o[j][1] *= back[0]; o[j][2] *= back[1]; o[j][3] *= back[1];
             }
         }
-        const float(*out)[4] = DELTA ? o : acc;
+        const float(*out)[4] = DELTA ? o : accp;
         row_scales<8>(out, 2 * m + 2, scale, back);
-        put_tiles<8>(out, 2 * m + 2, scale, sq.p, m);
+        put_tiles<8>(out, 2 * m + 2, scale, sq.a, m);
         if (c == 0) {
             sq.p_back[16 * m + g] = back[0];
             sq.p_back[16 * m + g + 8] = back[1];
@@ -359,7 +359,7 @@ template <bool DELTA>
 __device__ __forceinline__ void put_squares(const Squares &sq, uint8_t *inv_image, uint8_t *p_image)
 {
     if (DELTA) bulk_s2g(inv_image, sq.t, kSquareBytes);
-    bulk_s2g(p_image, sq.p, kSquareBytes);
+    bulk_s2g(p_image, sq.a, kSquareBytes);
     bulk_commit();
 }
 
@@ -379,157 +379,165 @@ __device__ __forceinline__ bool find_block(const PromptArgs &a, int first_block,
 }
 
 // ---------------------------------------------------------------------------
-// One gate a head.  A CTA takes a block and a query / key head: K K^T and Q K^T
-// on the tensor cores (warps 0-3 and 4-7, 16 rows each), then for each value
-// head of the group the decays, the inverse and the squares.  The decay from
+// One gate a head.  A CTA of four warps takes a block and a value head: K K^T and
+// Q K^T on the tensor cores (16 rows a warp), the decays, the inverse and the
+// squares.  Most of it is a chain of short steps, so what counts is how many
+// CTAs lie side by side on an SM; value heads that share a query / key head make
+// its products anew, and the first of them writes its operands.  The decay from
 // token s to token t is the product of what is left of s at the end of its 16
 // tokens, of the 16s between, and of t's 16 up to t; inside 16 tokens it is
 // multiplied out.
 // ---------------------------------------------------------------------------
+constexpr int kTileThreads = 128;
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dev::smem_addr(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+
+// Where the 16-byte piece `part` of a row lies before the row is split: in the
+// bytes of the row's halves.
+template <class T>
+__device__ __forceinline__ int raw_at(int row, int part)
+{
+    if constexpr (sizeof(T) == 2) return tile_at(row, 8 * part);
+    return (part >> 4) * kTileBytes + ((part >> 3) & 1) * (kTileBytes / 2) + row * 128 + (part & 7) * 16;
+}
+
 template <class T, int V, int NP>
-__global__ void __launch_bounds__(256) k_block_tiles(PromptArgs a, int first_block, Scratch sc)
+__global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(PromptArgs a, int first_block, Scratch sc)
 {
     extern __shared__ __align__(128) char smem[];
     __shared__ float ek[kC], eq[kC], s_beta[kC], s_pre[kC], s_suf[kC], s_blk[4], s_diag[4][16][17];
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
-    const int heads_k = a.heads / a.share;
     Block k;
-    const int hq = blockIdx.x % heads_k;
-    if (!find_block(a, first_block, blockIdx.x / heads_k, &k)) return;
-    // the gates of the first value head, while the tiles are made
+    const int h = blockIdx.x % a.heads, hq = h / a.share;
+    if (!find_block(a, first_block, blockIdx.x / a.heads, &k)) return;
     const int tok = tid & (kC - 1);
-    const bool in = tok < k.n;
-    const long long gate0 = (long long)(k.t0 + (in ? tok : 0)) * a.heads + hq * a.share;
     float alpha = 1.f, beta = 0.f;
-    if (in) {
-        alpha = a.alpha[gate0];
-        beta = a.beta[gate0];
+    if (tok < k.n) {
+        alpha = a.alpha[(long long)(k.t0 + tok) * a.heads + h];
+        beta = a.beta[(long long)(k.t0 + tok) * a.heads + h];
     }
+    // the rows as they are, into the places of their halves
     char *tk = smem, *tq = smem + NP * kTileBytes;
-    {
-        const T *kg = static_cast<const T *>(a.k) + hq * kDK, *qg = static_cast<const T *>(a.q) + hq * kDK;
-        constexpr bool exact = std::is_same<T, __half>::value;
-        float4 xk[kC / 8], xq[kC / 8];
+    const T *kg = static_cast<const T *>(a.k) + (long long)k.t0 * a.stride_k + hq * kDK, *qg = static_cast<const T *>(a.q) + (long long)k.t0 * a.stride_q + hq * kDK;
+    constexpr int pieces = kDK * sizeof(T) / 16;  // of a row
 #pragma unroll
-        for (int i = 0; i < kC / 8; i++) {
-            const int row = 8 * w + i;
-            xk[i] = xq[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row < k.n) {
-                xk[i] = load4(kg + (long long)(k.t0 + row) * a.stride_k + 4 * l);
-                xq[i] = load4(qg + (long long)(k.t0 + row) * a.stride_q + 4 * l);
-            }
+    for (int i = 0; i < kC * pieces / kTileThreads; i++) {
+        const int x = i * kTileThreads + tid, row = x / pieces, part = x % pieces, from = min(row, k.n - 1);
+        const int at = raw_at<T>(row, part);
+        cp_async16(tk + at, kg + from * a.stride_k + part * (16 / (int)sizeof(T)), row < k.n);
+        cp_async16(tq + at, qg + from * a.stride_q + part * (16 / (int)sizeof(T)), row < k.n);
+    }
+    if (tid < kC) {
+        float p = alpha, q = __shfl_down_sync(kFull, alpha, 1, 16);
+        if ((l & 15) == 15) q = 1.f;
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) {
+            const float x = __shfl_up_sync(kFull, p, d, 16), y = __shfl_down_sync(kFull, q, d, 16);
+            if ((l & 15) >= d) p *= x;
+            if ((l & 15) + d < 16) q *= y;
         }
+        s_pre[tid] = p;
+        s_suf[tid] = q;
+        s_beta[tid] = beta;
+        if ((l & 15) == 15) s_blk[tid >> 4] = p;
+    } else {
+        float p = 1.f;
 #pragma unroll
-        for (int i = 0; i < kC / 8; i++) {
-            const int row = 8 * w + i;
-            const float bk = put_row<NP, exact>(xk[i], row, l, tk), bq = put_row<NP, exact>(xq[i], row, l, tq);
+        for (int t = 0; t < 16; t++) {
+            const float x = __shfl_sync(kFull, alpha, t, 16);
+            if (t > (l & 15)) p *= x;
+            s_diag[tok >> 4][t][l & 15] = p;
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    if constexpr (std::is_same<T, __half>::value) {  // binary16 rows are their own halves
+        if (tid < kC) ek[tid] = eq[tid] = 1.f;
+    } else {
+#pragma unroll 4
+        for (int i = 0; i < 16; i++) {
+            const int row = 16 * w + i;
+            const float4 x = load4(reinterpret_cast<const T *>(tk + raw_at<T>(row, 4 * l * (int)sizeof(T) / 16)) + 4 * l % (16 / (int)sizeof(T))),
+                         y = load4(reinterpret_cast<const T *>(tq + raw_at<T>(row, 4 * l * (int)sizeof(T) / 16)) + 4 * l % (16 / (int)sizeof(T)));
+            __syncwarp();
+            const float bk = put_row<NP, false>(x, row, l, tk), bq = put_row<NP, false>(y, row, l, tq);
             if (l == 0) {
                 ek[row] = bk;
                 eq[row] = bq;
             }
         }
     }
-    fence_async();
+    const bool writes = h % a.share == 0;
+    if (writes) fence_async();
     __syncthreads();
-    if (tid == 0) {
-        const size_t at = ((size_t)k.b * heads_k + hq) * NP * kTileBytes;
+    if (tid == 0 && writes) {
+        const size_t at = ((size_t)k.b * (a.heads / a.share) + hq) * NP * kTileBytes;
         bulk_s2g(a.scratch + sc.k + at, tk, NP * kTileBytes);
         bulk_s2g(a.scratch + sc.q + at, tq, NP * kTileBytes);
         bulk_commit();
     }
-    const int m = w & 3;  // rows 16 m + g, + 8
-    const bool is_q = w >= 4;
-    float raw[kC / 8][4] = {};
-    if (is_q || V != kLinear) rows_product<NP>(raw, is_q ? tq : tk, tk, m, 2 * m + 2);
-    {
-        const float r0 = (is_q ? eq : ek)[16 * m + g], r1 = (is_q ? eq : ek)[16 * m + g + 8];
+    const int m = w;  // rows 16 m + g, + 8
+    const float b0 = s_beta[16 * m + g], b1 = s_beta[16 * m + g + 8];
+    // the products times the rows' unscales and the decays (and, for A, beta)
+    auto decayed = [&](float (*x)[4], bool is_q) {
+        const float *er = is_q ? eq : ek;
+        const float r0 = er[16 * m + g] * (is_q ? 1.f : b0), r1 = er[16 * m + g + 8] * (is_q ? 1.f : b1);
+        float f0 = s_pre[16 * m + g] * r0, f1 = s_pre[16 * m + g + 8] * r1;
 #pragma unroll
-        for (int j = 0; j < kC / 8; j++) {
-            const float c0 = ek[8 * j + 2 * c], c1 = ek[8 * j + 2 * c + 1];
-            raw[j][0] *= r0 * c0; raw[j][1] *= r0 * c1; raw[j][2] *= r1 * c0; raw[j][3] *= r1 * c1;
+        for (int jb = kC / 16 - 1; jb >= 0; jb--) {
+            if (jb > m) continue;
+            if (jb + 1 < m) {  // another 16 tokens between
+                f0 *= s_blk[jb + 1];
+                f1 *= s_blk[jb + 1];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int s = 16 * jb + 8 * e + 2 * c, si = 8 * e + 2 * c;
+                float *y = x[2 * jb + e];
+                const float2 u = *reinterpret_cast<const float2 *>(&ek[s]);
+                if (jb == m) {
+                    const int d = is_q ? 0 : 1;  // P has its diagonal, A does not
+                    y[0] = si + d <= g ? y[0] * (s_diag[m][g][si] * r0 * u.x) : 0.f;
+                    y[1] = si + 1 + d <= g ? y[1] * (s_diag[m][g][si + 1] * r0 * u.y) : 0.f;
+                    y[2] = si + d <= g + 8 ? y[2] * (s_diag[m][g + 8][si] * r1 * u.x) : 0.f;
+                    y[3] = si + 1 + d <= g + 8 ? y[3] * (s_diag[m][g + 8][si + 1] * r1 * u.y) : 0.f;
+                } else {
+                    const float2 q = *reinterpret_cast<const float2 *>(&s_suf[s]);
+                    y[0] *= f0 * q.x * u.x; y[1] *= f0 * q.y * u.y;
+                    y[2] *= f1 * q.x * u.x; y[3] *= f1 * q.y * u.y;
+                }
+            }
         }
-    }
+    };
+    float acc[kC / 8][4] = {}, accp[kC / 8][4] = {};
+    rows_product<NP>(accp, tq, tk, m, 2 * m + 2);
+    if (V != kLinear) rows_product<NP>(acc, tk, tk, m, 2 * m + 2);
+    if (tid == 0 && writes) bulk_wait_read();
+    __syncthreads();
     // the tiles are done with: their room holds the squares
     Squares &sq = *reinterpret_cast<Squares *>(smem);
-    for (int v = 0; v < a.share; v++) {
-        const int h = hq * a.share + v;
-        __syncthreads();  // the vectors of the head before are read
-        if (tid < kC) {
-            float p = alpha, q = __shfl_down_sync(kFull, alpha, 1, 16);
-            if ((l & 15) == 15) q = 1.f;
-#pragma unroll
-            for (int d = 1; d < 16; d <<= 1) {
-                const float x = __shfl_up_sync(kFull, p, d, 16), y = __shfl_down_sync(kFull, q, d, 16);
-                if ((l & 15) >= d) p *= x;
-                if ((l & 15) + d < 16) q *= y;
-            }
-            s_pre[tid] = p;
-            s_suf[tid] = q;
-            s_beta[tid] = beta;
-            if ((l & 15) == 15) s_blk[tid >> 4] = p;
-        } else if (tid < 2 * kC) {
-            float p = 1.f;
-#pragma unroll
-            for (int t = 0; t < 16; t++) {
-                const float x = __shfl_sync(kFull, alpha, t, 16);
-                if (t > (l & 15)) p *= x;
-                s_diag[tok >> 4][t][l & 15] = p;
-            }
-        }
-        if (v + 1 < a.share && in) {
-            alpha = a.alpha[gate0 + v + 1];
-            beta = a.beta[gate0 + v + 1];
-        }
-        if (tid == 0) bulk_wait_read();  // the tiles, or the squares before, are copied
-        __syncthreads();
-        float acc[kC / 8][4];
-        {
-            const int i0 = g, i1 = g + 8;  // rows within the block of 16
-            const float b0 = is_q ? 1.f : s_beta[16 * m + i0], b1 = is_q ? 1.f : s_beta[16 * m + i1];
-            float f0 = s_pre[16 * m + i0] * b0, f1 = s_pre[16 * m + i1] * b1;
-#pragma unroll
-            for (int jb = kC / 16 - 1; jb >= 0; jb--) {
-                if (jb + 1 < m) {  // another 16 tokens between
-                    f0 *= s_blk[jb + 1];
-                    f1 *= s_blk[jb + 1];
-                }
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const int j = 2 * jb + e, s = 8 * j + 2 * c, si = s & 15;
-                    float *x = acc[j];
-                    if (jb > m) {
-                        x[0] = x[1] = x[2] = x[3] = 0.f;
-                    } else if (jb == m) {
-                        x[0] = (is_q ? si <= i0 : si < i0) ? raw[j][0] * s_diag[m][i0][si] * b0 : 0.f;
-                        x[1] = (is_q ? si + 1 <= i0 : si + 1 < i0) ? raw[j][1] * s_diag[m][i0][si + 1] * b0 : 0.f;
-                        x[2] = (is_q ? si <= i1 : si < i1) ? raw[j][2] * s_diag[m][i1][si] * b1 : 0.f;
-                        x[3] = (is_q ? si + 1 <= i1 : si + 1 < i1) ? raw[j][3] * s_diag[m][i1][si + 1] * b1 : 0.f;
-                    } else {
-                        const float2 q = *reinterpret_cast<const float2 *>(&s_suf[s]);
-                        x[0] = raw[j][0] * (f0 * q.x); x[1] = raw[j][1] * (f0 * q.y);
-                        x[2] = raw[j][2] * (f1 * q.x); x[3] = raw[j][3] * (f1 * q.y);
-                    }
-                }
-            }
-        }
-        const size_t bh = (size_t)k.b * a.heads + h;
-        finish<V != kLinear>(acc, sq);
-        if (tid == 0) put_squares<V != kLinear>(sq, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
-        if (tid < kC) {
-            float *sv = reinterpret_cast<float *>(a.scratch + sc.sv) + bh * kStateFloats;
-            float *ov = reinterpret_cast<float *>(a.scratch + sc.ov) + bh * kOutFloats;
-            const int b = tid >> 4;
-            float ct = s_pre[tid], left = s_suf[tid];
-            for (int i = 0; i < b; i++) ct *= s_blk[i];
-            for (int i = b + 1; i < 4; i++) left *= s_blk[i];
-            left *= ek[tid];
-            sv[tid] = -s_beta[tid] * ct * ek[tid];
-            sv[kC + tid] = s_beta[tid];
-            sv[2 * kC + tid] = V == kLinear ? left : sq.t_back[tid] * left;
-            if (tid == kC - 1) sv[3 * kC] = ct;
-            ov[tid] = ct * eq[tid];
-            ov[kC + tid] = sq.p_back[tid];
-        }
+    decayed(accp, true);
+    if (V != kLinear) decayed(acc, false);
+    finish<V != kLinear>(acc, accp, sq);
+    const size_t bh = (size_t)k.b * a.heads + h;
+    if (tid == 0) put_squares<V != kLinear>(sq, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
+    if (tid < kC) {
+        float *sv = reinterpret_cast<float *>(a.scratch + sc.sv) + bh * kStateFloats;
+        float *ov = reinterpret_cast<float *>(a.scratch + sc.ov) + bh * kOutFloats;
+        const int b = tid >> 4;
+        float ct = s_pre[tid], left = s_suf[tid];
+        for (int i = 0; i < b; i++) ct *= s_blk[i];
+        for (int i = b + 1; i < 4; i++) left *= s_blk[i];
+        left *= ek[tid];
+        sv[tid] = -s_beta[tid] * ct * ek[tid];
+        sv[kC + tid] = s_beta[tid];
+        sv[2 * kC + tid] = V == kLinear ? left : sq.t_back[tid] * left;
+        if (tid == kC - 1) sv[3 * kC] = ct;
+        ov[tid] = ct * eq[tid];
+        ov[kC + tid] = sq.p_back[tid];
     }
     if (tid == 0) bulk_wait();
 }
@@ -717,16 +725,19 @@ __global__ void __launch_bounds__(kGateThreads) k_gate_tiles(PromptArgs a, int f
     __syncthreads();
     // everything but A and P is done with: the squares take its room
     Squares &squares = *reinterpret_cast<Squares *>(smem);
-    float acc[kC / 8][4] = {};
-    if (w < 8) {
-        const float *src = (w < 4 ? sA : sP) + 16 * (w & 3) * kLd;
+    float acc[kC / 8][4] = {}, accp[kC / 8][4] = {};
+    if (w < 4) {
+        auto fetch = [&](float (*x)[4], const float *src) {
 #pragma unroll
-        for (int j = 0; j < kC / 8; j++) {
-            const float2 x = *reinterpret_cast<const float2 *>(src + g * kLd + 8 * j + 2 * c), y = *reinterpret_cast<const float2 *>(src + (g + 8) * kLd + 8 * j + 2 * c);
-            acc[j][0] = x.x; acc[j][1] = x.y; acc[j][2] = y.x; acc[j][3] = y.y;
-        }
+            for (int j = 0; j < kC / 8; j++) {
+                const float2 y = *reinterpret_cast<const float2 *>(src + (16 * w + g) * kLd + 8 * j + 2 * c), z = *reinterpret_cast<const float2 *>(src + (16 * w + g + 8) * kLd + 8 * j + 2 * c);
+                x[j][0] = y.x; x[j][1] = y.y; x[j][2] = z.x; x[j][3] = z.y;
+            }
+        };
+        fetch(acc, sA);
+        fetch(accp, sP);
     }
-    finish<true>(acc, squares);
+    finish<true>(acc, accp, squares);
     if (tid == 0) put_squares<true>(squares, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
     float *sv = reinterpret_cast<float *>(a.scratch + sc.sv) + bh * kStateFloats;
     if (tid < kC) {
@@ -749,7 +760,7 @@ cudaError_t launch_tiles(const PromptArgs &a, int first, int n, const Scratch &s
     const int dyn = std::max(2 * NP * kTileBytes, (int)sizeof(Squares));
     cudaError_t e = cudaFuncSetAttribute(k_block_tiles<T, V, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, dyn);
     if (e != cudaSuccess) return e;
-    k_block_tiles<T, V, NP><<<(unsigned)n * (unsigned)(a.heads / a.share), 256, dyn, s>>>(a, first, sc);
+    k_block_tiles<T, V, NP><<<(unsigned)n * (unsigned)a.heads, kTileThreads, dyn, s>>>(a, first, sc);
     return cudaGetLastError();
 }
 
