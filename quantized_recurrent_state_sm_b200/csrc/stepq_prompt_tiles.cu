@@ -109,7 +109,7 @@ __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, con
 // ---- the inverse and the squares ---------------------------------------------
 //
 // A (strictly lower triangular, [64][64]) and P are held as accumulators: warp m
-// of 0-3 has rows 16 m .. of both, all columns.  With T = (I +
+// of 0-3 has rows 16 m .. of A, all columns, and warp m or m + 4 those of P.  With T = (I +
 // A)^-1 in blocks of 16: T_mm by substitution, then row by row
 //   T_m = T_mm - (T_mm A_m) T_(<m),
 // products on the tensor cores; P T likewise.  A left operand comes from the
@@ -199,10 +199,9 @@ __device__ __forceinline__ void times_square(float (*out)[4], const float (*x)[4
     }
 }
 
-// From A and P (the accumulators of warps 0-3, zero above the diagonal) to the
-// halves of T and P T in sq.  Warps past the fourth only meet the barriers.
-// Ends with a barrier.
-template <bool DELTA>
+// From A and P (the accumulators of warps 0-3 and PW .. PW + 3, zero above the
+// diagonal) to the halves of T and P T in sq.  Ends with a barrier.
+template <bool DELTA, int PW>
 __device__ __forceinline__ void finish(float (*acc)[4], float (*accp)[4], Squares &sq)
 {
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3, m = w & 3;
@@ -326,7 +325,7 @@ __device__ __forceinline__ void finish(float (*acc)[4], float (*accp)[4], Square
             __syncthreads();
         }
     }
-    if (w < 4) {
+    if (w >= PW && w < PW + 4) {
         float o[8][4] = {};
         if constexpr (DELTA) {
 #pragma unroll
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
     Squares &sq = *reinterpret_cast<Squares *>(smem);
     decayed(accp, true);
     if (V != kLinear) decayed(acc, false);
-    finish<V != kLinear>(acc, accp, sq);
+    finish<V != kLinear, 0>(acc, accp, sq);
     const size_t bh = (size_t)k.b * a.heads + h;
     if (tid == 0) put_squares<V != kLinear>(sq, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
     if (tid < kC) {
@@ -547,76 +546,148 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
 // from row to row, so no product of K and Q alone serves: between blocks of 16
 // tokens the rows are multiplied by what is left of them at the blocks' border
 // (all factors at most 1 for gates at most 1) and then go to the tensor cores,
-// inside 16 tokens the sums run over the multiplied-out decays.
+// inside 16 tokens the sums run over the multiplied-out decays.  Gates, K and Q
+// are held in fp32, and give their places to the multiplied rows: what is needed
+// of shared memory decides how many CTAs lie side by side (two).
 // ---------------------------------------------------------------------------
-constexpr int kGateThreads = 512;
-constexpr int kRowLd = kDK + 8;  // row of a [64][128] fp32 matrix: fragments of 8 rows x 8 columns fall into different banks
-constexpr int kLd = kC + 8;          // row of a [64][64] fp32 matrix
-constexpr int kGateBytes = (5 * kC * kRowLd + 2 * kC * kLd) * 4;
+constexpr int kGateThreads = 256;
+constexpr int kRowLd = kDK + 4;  // row of a [64][128] fp32 matrix
+struct GateRows {
+    __align__(128) float a[kC][kRowLd], k[kC][kRowLd], q[kC][kRowLd];  // gates, K, Q; then K times what is left, K and Q times what was kept
+    float diag_a[4][16][17], diag_p[4][16][17];  // A and P inside 16 tokens
+    float blk[4][kDK];                           // products of 16 tokens' gates
+    float ek[kC], eq[kC], ek2[kC], beta[kC];
+    float ks[kC], kb[kC], qs[kC], qb[kC];        // scale and unscale of the rows of K and Q
+};
+static_assert(sizeof(GateRows) <= 115712 && sizeof(Squares) <= sizeof(GateRows::a) + sizeof(GateRows::k), "two CTAs of an SM; room for the squares");
 
 __device__ __forceinline__ float4 mul4(float4 x, float4 y) { return make_float4(x.x * y.x, x.y * y.y, x.z * y.z, x.w * y.w); }
+__device__ __forceinline__ float4 at4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
 template <class T>
-__global__ void __launch_bounds__(kGateThreads) k_gate_tiles(PromptArgs a, int first_block, Scratch sc)
+__global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, int first_block, Scratch sc)
 {
     extern __shared__ __align__(128) char smem[];
-    __shared__ float ek[kC], eq[kC], ek2[kC], s_beta[kC];
-    __shared__ float s_ks[kC], s_kb[kC], s_qs[kC], s_qb[kC];  // scale and unscale of the rows of K and Q
-    __shared__ __align__(16) float s_blk[4][kDK];
-    float *sa = reinterpret_cast<float *>(smem), *sk = sa + kC * kRowLd, *sq = sk + kC * kRowLd, *pre = sq + kC * kRowLd, *suf = pre + kC * kRowLd;
-    float *sA = suf + kC * kRowLd, *sP = sA + kC * kLd;
+    GateRows &r = *reinterpret_cast<GateRows *>(smem);
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
     Block k;
-    const int h = blockIdx.x % a.heads;
+    const int h = blockIdx.x % a.heads, hq = h / a.share;
     if (!find_block(a, first_block, blockIdx.x / a.heads, &k)) return;
-    const int hq = h / a.share;
-    // gates of 16 tokens of a key row a thread: running products from the 16's
-    // start, and what is left at its end
     {
-        const int b = tid >> 7, d = tid & (kDK - 1);
-        const float *ag = a.alpha + ((long long)(k.t0 + 16 * b) * a.heads + h) * kDK + d;
-        float x[16];
+        const float *ag = a.alpha + ((long long)k.t0 * a.heads + h) * kDK;
+        for (int x = tid; x < kC * (kDK / 4); x += kGateThreads) {
+            const int row = x / (kDK / 4), d = x % (kDK / 4) * 4;
+            if (row < k.n)
+                cp_async16(&r.a[row][d], ag + (long long)row * a.heads * kDK + d, true);
+            else
+                *reinterpret_cast<float4 *>(&r.a[row][d]) = make_float4(1.f, 1.f, 1.f, 1.f);
+        }
+        const T *kg = static_cast<const T *>(a.k) + (long long)k.t0 * a.stride_k + hq * kDK + 4 * l, *qg = static_cast<const T *>(a.q) + (long long)k.t0 * a.stride_q + hq * kDK + 4 * l;
+        float4 x[8], y[8];
 #pragma unroll
-        for (int i = 0; i < 16; i++) x[i] = 16 * b + i < k.n ? ag[(long long)i * a.heads * kDK] : 1.f;
+        for (int i = 0; i < 8; i++) {
+            const int row = 8 * w + i;
+            x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < k.n) {
+                x[i] = load4(kg + row * a.stride_k);
+                y[i] = load4(qg + row * a.stride_q);
+            }
+        }
+        if (tid < kC) r.beta[tid] = tid < k.n ? a.beta[(long long)(k.t0 + tid) * a.heads + h] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int row = 8 * w + i;
+            *reinterpret_cast<float4 *>(&r.k[row][4 * l]) = x[i];
+            *reinterpret_cast<float4 *>(&r.q[row][4 * l]) = y[i];
+            float s, b, s2, b2;
+            dev::row_scale(warp_max(x[i]), &s, &b);
+            dev::row_scale(warp_max(y[i]), &s2, &b2);
+            if (l == 0) {
+                r.ks[row] = s; r.kb[row] = b;
+                r.qs[row] = s2; r.qb[row] = b2;
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    __syncthreads();
+    // inside 16 tokens: a warp takes four columns s at a time, four key rows a
+    // lane, and walks down the rows t; two turns of four columns, a long and a
+    // short one
+#pragma unroll 1
+    for (int turn = 0; turn < 2; turn++) {
+        const int b = w >> 1, i0 = (w & 1) ? 4 + 4 * turn : 12 * turn, first = 16 * b;
+        float2 x[4][2];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const float4 y = at4(&r.k[first + i0 + u][4 * l]);
+            x[u][0] = make_float2(y.x, y.y);
+            x[u][1] = make_float2(y.z, y.w);
+        }
+#pragma unroll 1
+        for (int t = i0; t < 16; t++) {
+            const float4 al = at4(&r.a[first + t][4 * l]), y = at4(&r.k[first + t][4 * l]), z = at4(&r.q[first + t][4 * l]);
+            const float2 a0 = make_float2(al.x, al.y), a1 = make_float2(al.z, al.w), y0 = make_float2(y.x, y.y), y1 = make_float2(y.z, y.w),
+                         z0 = make_float2(z.x, z.y), z1 = make_float2(z.z, z.w);
+            float v[8];  // sums of the four columns with K, then with Q
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                if (t > i0 + u) {
+                    x[u][0] = __fmul2_rn(x[u][0], a0);
+                    x[u][1] = __fmul2_rn(x[u][1], a1);
+                }
+                const float2 p = __ffma2_rn(x[u][1], y1, __fmul2_rn(x[u][0], y0)), q = __ffma2_rn(x[u][1], z1, __fmul2_rn(x[u][0], z0));
+                v[u] = p.x + p.y;
+                v[4 + u] = q.x + q.y;
+            }
+            // eight sums over 32 lanes: each exchange halves the values a lane keeps
+#pragma unroll
+            for (int n = 4; n >= 1; n >>= 1) {
+                const bool up = l & (4 * n);
+#pragma unroll
+                for (int i = 0; i < n; i++) {
+                    const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+                    v[i] = keep + __shfl_xor_sync(kFull, give, 4 * n);
+                }
+            }
+            v[0] += __shfl_xor_sync(kFull, v[0], 2);
+            v[0] += __shfl_xor_sync(kFull, v[0], 1);
+            if (c == 0) {  // lane bits 4, 3, 2: K or Q, and the column
+                const int s = i0 + (g & 3);
+                if (g < 4)
+                    r.diag_a[b][t][s] = t > s ? v[0] * r.beta[first + t] : 0.f;
+                else
+                    r.diag_p[b][t][s] = t >= s ? v[0] : 0.f;
+            }
+        }
+        // the rows above
+        if (l < i0) {
+#pragma unroll
+            for (int u = 0; u < 4; u++) r.diag_a[b][l][i0 + u] = r.diag_p[b][l][i0 + u] = 0.f;
+        }
+    }
+    __syncthreads();
+    // gates of 16 tokens of a key row: what is kept from the 16's start, and what
+    // is left at its end
+#pragma unroll 1
+    for (int x = tid; x < 4 * kDK; x += kGateThreads) {
+        const int b = x / kDK, d = x % kDK;
+        float al[16], kk[16];
         float p = 1.f;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-            const int at = (16 * b + i) * kRowLd + d;
-            p *= x[i];
-            sa[at] = x[i];
-            pre[at] = p;
+            al[i] = r.a[16 * b + i][d];
+            kk[i] = r.k[16 * b + i][d];
+            p *= al[i];
+            r.k[16 * b + i][d] = kk[i] * p;
+            r.q[16 * b + i][d] *= p;
         }
-        s_blk[b][d] = p;
+        r.blk[b][d] = p;
         p = 1.f;
 #pragma unroll
         for (int i = 15; i >= 0; i--) {
-            suf[(16 * b + i) * kRowLd + d] = p;
-            p *= x[i];
+            r.a[16 * b + i][d] = kk[i] * p;
+            p *= al[i];
         }
-    }
-    {
-        const T *kg = static_cast<const T *>(a.k) + hq * kDK, *qg = static_cast<const T *>(a.q) + hq * kDK;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int row = 4 * w + i;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-            if (row < k.n) {
-                x = load4(kg + (long long)(k.t0 + row) * a.stride_k + 4 * l);
-                y = load4(qg + (long long)(k.t0 + row) * a.stride_q + 4 * l);
-            }
-            *reinterpret_cast<float4 *>(sk + row * kRowLd + 4 * l) = x;
-            *reinterpret_cast<float4 *>(sq + row * kRowLd + 4 * l) = y;
-            float s, b, s2, b2;
-            dev::row_scale(warp_max(x), &s, &b);
-            dev::row_scale(warp_max(y), &s2, &b2);
-            if (l == 0) {
-                s_ks[row] = s; s_kb[row] = b;
-                s_qs[row] = s2; s_qb[row] = b2;
-            }
-        }
-        if (tid < kC) s_beta[tid] = tid < k.n ? a.beta[(long long)(k.t0 + tid) * a.heads + h] : 0.f;
-        // zeros above the diagonal
-        for (int i = tid; i < kC * kLd; i += kGateThreads) sA[i] = sP[i] = 0.f;
     }
     __syncthreads();
     // the operands that meet the state: K and Q times the running products, K
@@ -624,132 +695,100 @@ __global__ void __launch_bounds__(kGateThreads) k_gate_tiles(PromptArgs a, int f
     const size_t bh = (size_t)k.b * a.heads + h;
     {
         char *img = reinterpret_cast<char *>(a.scratch) + bh * 2 * kTileBytes;
-        const int b = w >> 2;  // the 16 tokens of this warp's rows
+        const int b = w >> 1;  // the 16 tokens of this warp's rows
         float4 before = make_float4(1.f, 1.f, 1.f, 1.f), behind = before;
-        for (int i = 0; i < b; i++) before = mul4(before, *reinterpret_cast<const float4 *>(&s_blk[i][4 * l]));
-        for (int i = b + 1; i < 4; i++) behind = mul4(behind, *reinterpret_cast<const float4 *>(&s_blk[i][4 * l]));
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int row = 4 * w + i, at = row * kRowLd + 4 * l;
-            const float4 ct = mul4(before, *reinterpret_cast<const float4 *>(pre + at)), left = mul4(behind, *reinterpret_cast<const float4 *>(suf + at));
-            const float4 x = *reinterpret_cast<const float4 *>(sk + at), y = *reinterpret_cast<const float4 *>(sq + at);
-            const float b0 = put_row<2, false>(mul4(x, ct), row, l, img + sc.k), b1 = put_row<2, false>(mul4(y, ct), row, l, img + sc.q),
-                        b2 = put_row<2, false>(mul4(x, left), row, l, img + sc.k2);
+        for (int i = 0; i < b; i++) before = mul4(before, at4(&r.blk[i][4 * l]));
+        for (int i = b + 1; i < 4; i++) behind = mul4(behind, at4(&r.blk[i][4 * l]));
+#pragma unroll 4
+        for (int i = 0; i < 8; i++) {
+            const int row = 8 * w + i;
+            const float b0 = put_row<2, false>(mul4(at4(&r.k[row][4 * l]), before), row, l, img + sc.k),
+                        b1 = put_row<2, false>(mul4(at4(&r.q[row][4 * l]), before), row, l, img + sc.q),
+                        b2 = put_row<2, false>(mul4(at4(&r.a[row][4 * l]), behind), row, l, img + sc.k2);
             if (l == 0) {
-                ek[row] = b0;
-                eq[row] = b1;
-                ek2[row] = b2;
+                r.ek[row] = b0;
+                r.eq[row] = b1;
+                r.ek2[row] = b2;
             }
         }
     }
-    // rows of 16 tokens i against those of an earlier 16 j, K by warps 0-5, Q by 6-11
-    if (w < 12) {
-        const int task = w % 6, i = task < 1 ? 1 : (task < 3 ? 2 : 3), j = task - (i == 1 ? 0 : (i == 2 ? 1 : 3));
-        const bool is_q = w >= 6;
-        const float *src = is_q ? sq : sk;
-        const int r0 = 16 * i + g, r1 = r0 + 8;
-        const float s0 = (is_q ? s_qs : s_ks)[r0], s1 = (is_q ? s_qs : s_ks)[r1];
-        const int c0 = 16 * j + g, c1 = c0 + 8;  // right rows of the two column tiles
-        const float k0 = s_ks[c0], k1 = s_ks[c1];
-        float acc[2][4] = {};
-        auto pair = [&](const float *x, const float *y, int row, int col, float scale) {
-            const float2 u = *reinterpret_cast<const float2 *>(x + row * kRowLd + col), v = *reinterpret_cast<const float2 *>(y + row * kRowLd + col);
-            return make_float2(u.x * v.x * scale, u.y * v.y * scale);
-        };
-#pragma unroll
-        for (int ks = 0; ks < kDK / 16; ks++) {
-            uint32_t ah[4], al[4];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int col = 16 * ks + 8 * e + 2 * c;
-                dev::split_half(pair(src, pre, r0, col, s0), &ah[2 * e], &al[2 * e]);
-                dev::split_half(pair(src, pre, r1, col, s1), &ah[2 * e + 1], &al[2 * e + 1]);
-            }
-            uint32_t bh_[2][2], bl[2][2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int col = 16 * ks + 8 * e + 2 * c;
-                float2 x = pair(sk, suf, c0, col, k0), y = pair(sk, suf, c1, col, k1);
-                for (int b = j + 1; b < i; b++) {  // the 16s between
-                    const float2 f = *reinterpret_cast<const float2 *>(&s_blk[b][col]);
-                    x.x *= f.x; x.y *= f.y; y.x *= f.x; y.y *= f.y;
-                }
-                dev::split_half(x, &bh_[0][e], &bl[0][e]);
-                dev::split_half(y, &bh_[1][e], &bl[1][e]);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; e++) mma16816(acc[e], al[0], al[1], al[2], al[3], bh_[e][0], bh_[e][1]);
-#pragma unroll
-            for (int e = 0; e < 2; e++) mma16816(acc[e], ah[0], ah[1], ah[2], ah[3], bl[e][0], bl[e][1]);
-#pragma unroll
-            for (int e = 0; e < 2; e++) mma16816(acc[e], ah[0], ah[1], ah[2], ah[3], bh_[e][0], bh_[e][1]);
-        }
-        float *dst = is_q ? sP : sA;
-        const float f0 = is_q ? s_qb[r0] : s_kb[r0] * s_beta[r0], f1 = is_q ? s_qb[r1] : s_kb[r1] * s_beta[r1];
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            const int s = 16 * j + 8 * e + 2 * c;
-            const float2 kb = *reinterpret_cast<const float2 *>(&s_kb[s]);
-            *reinterpret_cast<float2 *>(dst + r0 * kLd + s) = make_float2(acc[e][0] * (f0 * kb.x), acc[e][1] * (f0 * kb.y));
-            *reinterpret_cast<float2 *>(dst + r1 * kLd + s) = make_float2(acc[e][2] * (f1 * kb.x), acc[e][3] * (f1 * kb.y));
-        }
-    }
-    // inside 16 tokens: a warp takes four columns s of a block, eight lanes each
-    // over the key rows, and walks down the rows t
+    // rows of 16 tokens m against those of the earlier 16s, K by warps 0-3, Q by 4-7
+    const int m = w & 3;
+    const bool is_q = w >= 4;
+    float acc[kC / 8][4] = {};
     {
-        const int b = 16 * (w >> 2), i0 = 4 * (w & 3), s = b + i0 + (l >> 3), d0 = 4 * (l & 7);
-        float4 x[4];
+        const float(*src)[kRowLd] = is_q ? r.q : r.k;
+        const int r0 = 16 * m + g, r1 = r0 + 8;
+        const float s0 = (is_q ? r.qs : r.ks)[r0], s1 = (is_q ? r.qs : r.ks)[r1];
+        auto pair = [&](const float *row, int col, float scale) {
+            const float2 u = *reinterpret_cast<const float2 *>(row + col);
+            return make_float2(u.x * scale, u.y * scale);
+        };
+#pragma unroll 1
+        for (int ks = 0; ks < kDK / 16; ks++) {
+            if (m == 0) break;
+            uint32_t ah[4], al[4];
+            float2 between[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
 #pragma unroll
-        for (int i = 0; i < 4; i++) x[i] = *reinterpret_cast<const float4 *>(sk + s * kRowLd + d0 + 32 * i);
-        for (int t = b + i0; t < b + 16; t++) {
-            float ka = 0.f, qa = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int at = t * kRowLd + d0 + 32 * i;
-                if (t > s) x[i] = mul4(x[i], *reinterpret_cast<const float4 *>(sa + at));
-                const float4 y = *reinterpret_cast<const float4 *>(sk + at), z = *reinterpret_cast<const float4 *>(sq + at);
-                ka = fmaf(x[i].x, y.x, fmaf(x[i].y, y.y, fmaf(x[i].z, y.z, fmaf(x[i].w, y.w, ka))));
-                qa = fmaf(x[i].x, z.x, fmaf(x[i].y, z.y, fmaf(x[i].z, z.z, fmaf(x[i].w, z.w, qa))));
+            for (int e = 0; e < 2; e++) {
+                const int col = 16 * ks + 8 * e + 2 * c;
+                dev::split_half(pair(src[r0], col, s0), &ah[2 * e], &al[2 * e]);
+                dev::split_half(pair(src[r1], col, s1), &ah[2 * e + 1], &al[2 * e + 1]);
             }
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) {
-                ka += __shfl_xor_sync(kFull, ka, d);
-                qa += __shfl_xor_sync(kFull, qa, d);
+            for (int j = 2; j >= 0; j--) {
+                if (j >= m) continue;
+                uint32_t bh_[2][2], bl[2][2];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int col = 16 * ks + 8 * e + 2 * c;
+                    if (j + 1 < m) {  // another 16 tokens between
+                        const float2 f = *reinterpret_cast<const float2 *>(&r.blk[j + 1][col]);
+                        between[e].x *= f.x;
+                        between[e].y *= f.y;
+                    }
+                    const float2 x = pair(r.a[16 * j + g], col, r.ks[16 * j + g]), y = pair(r.a[16 * j + g + 8], col, r.ks[16 * j + g + 8]);
+                    dev::split_half(x.x * between[e].x, x.y * between[e].y, &bh_[0][e], &bl[0][e]);
+                    dev::split_half(y.x * between[e].x, y.y * between[e].y, &bh_[1][e], &bl[1][e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; e++) mma16816(acc[2 * j + e], al[0], al[1], al[2], al[3], bh_[e][0], bh_[e][1]);
+#pragma unroll
+                for (int e = 0; e < 2; e++) mma16816(acc[2 * j + e], ah[0], ah[1], ah[2], ah[3], bl[e][0], bl[e][1]);
+#pragma unroll
+                for (int e = 0; e < 2; e++) mma16816(acc[2 * j + e], ah[0], ah[1], ah[2], ah[3], bh_[e][0], bh_[e][1]);
             }
-            if ((l & 7) == 0) {
-                if (t > s) sA[t * kLd + s] = ka * s_beta[t];
-                if (t >= s) sP[t * kLd + s] = qa;
+        }
+        const float f0 = is_q ? r.qb[r0] : r.kb[r0] * r.beta[r0], f1 = is_q ? r.qb[r1] : r.kb[r1] * r.beta[r1];
+        const float(*diag)[17] = is_q ? r.diag_p[m] : r.diag_a[m];
+#pragma unroll
+        for (int j = 0; j < kC / 8; j++) {
+            const int s = 8 * j + 2 * c;
+            if (j < 2 * m) {
+                const float2 kb = *reinterpret_cast<const float2 *>(&r.kb[s]);
+                acc[j][0] *= f0 * kb.x; acc[j][1] *= f0 * kb.y; acc[j][2] *= f1 * kb.x; acc[j][3] *= f1 * kb.y;
+            } else if (j < 2 * m + 2) {
+                const int i = s & 15;
+                acc[j][0] = diag[g][i]; acc[j][1] = diag[g][i + 1]; acc[j][2] = diag[g + 8][i]; acc[j][3] = diag[g + 8][i + 1];
             }
         }
     }
     __syncthreads();
-    // everything but A and P is done with: the squares take its room
-    Squares &squares = *reinterpret_cast<Squares *>(smem);
-    float acc[kC / 8][4] = {}, accp[kC / 8][4] = {};
-    if (w < 4) {
-        auto fetch = [&](float (*x)[4], const float *src) {
-#pragma unroll
-            for (int j = 0; j < kC / 8; j++) {
-                const float2 y = *reinterpret_cast<const float2 *>(src + (16 * w + g) * kLd + 8 * j + 2 * c), z = *reinterpret_cast<const float2 *>(src + (16 * w + g + 8) * kLd + 8 * j + 2 * c);
-                x[j][0] = y.x; x[j][1] = y.y; x[j][2] = z.x; x[j][3] = z.y;
-            }
-        };
-        fetch(acc, sA);
-        fetch(accp, sP);
-    }
-    finish<true>(acc, accp, squares);
-    if (tid == 0) put_squares<true>(squares, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
+    // the rows are done with: their room holds the squares
+    Squares &sq = *reinterpret_cast<Squares *>(smem);
+    finish<true, 4>(acc, acc, sq);
+    if (tid == 0) put_squares<true>(sq, a.scratch + sc.inv + bh * kSquareBytes, a.scratch + sc.p + bh * kSquareBytes);
     float *sv = reinterpret_cast<float *>(a.scratch + sc.sv) + bh * kStateFloats;
     if (tid < kC) {
         float *ov = reinterpret_cast<float *>(a.scratch + sc.ov) + bh * kOutFloats;
-        sv[tid] = -s_beta[tid] * ek[tid];
-        sv[kC + tid] = s_beta[tid];
-        sv[2 * kC + tid] = squares.t_back[tid] * ek2[tid];
-        ov[tid] = eq[tid];
-        ov[kC + tid] = squares.p_back[tid];
-    } else if (tid >= 128 && tid < 128 + kDK) {
-        const int d = tid - 128;
-        sv[3 * kC + d] = s_blk[0][d] * s_blk[1][d] * s_blk[2][d] * s_blk[3][d];
+        sv[tid] = -r.beta[tid] * r.ek[tid];
+        sv[kC + tid] = r.beta[tid];
+        sv[2 * kC + tid] = sq.t_back[tid] * r.ek2[tid];
+        ov[tid] = r.eq[tid];
+        ov[kC + tid] = sq.p_back[tid];
+    } else if (tid >= kDK) {
+        const int d = tid - kDK;
+        sv[3 * kC + d] = r.blk[0][d] * r.blk[1][d] * r.blk[2][d] * r.blk[3][d];
     }
     if (tid == 0) bulk_wait();
 }
@@ -770,9 +809,9 @@ cudaError_t launch_tiles_v(const PromptArgs &a, int first, int n, const Scratch 
     constexpr int NP = sizeof(T) == 4 ? 2 : 1;
     if (a.variant == kGdn) return launch_tiles<T, kGdn, NP>(a, first, n, sc, s);
     if (a.variant == kLinear) return launch_tiles<T, kLinear, NP>(a, first, n, sc, s);
-    cudaError_t e = cudaFuncSetAttribute(k_gate_tiles<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGateBytes);
+    cudaError_t e = cudaFuncSetAttribute(k_gate_tiles<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(GateRows));
     if (e != cudaSuccess) return e;
-    k_gate_tiles<T><<<(unsigned)n * (unsigned)a.heads, kGateThreads, kGateBytes, s>>>(a, first, sc);
+    k_gate_tiles<T><<<(unsigned)n * (unsigned)a.heads, kGateThreads, sizeof(GateRows), s>>>(a, first, sc);
     return cudaGetLastError();
 }
 
