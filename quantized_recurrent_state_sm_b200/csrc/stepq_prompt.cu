@@ -51,19 +51,19 @@ __global__ void __launch_bounds__(kStepThreads) k_prompt_steps(PromptArgs a)
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
     const int slice = blockIdx.x % kStepSlices;
     const int item = blockIdx.x / kStepSlices, r = item / a.heads, h = item - r * a.heads;
-    const int live = a.p.live[r];
+    // one wait for all of the request's entries
+    const int live = a.p.live[r], t0 = a.p.starts[r], t1 = a.p.starts[r + 1];
+    const bool fresh = a.p.fresh[r] != 0;
     if (live < 0) return;
-    const int t0 = a.p.starts[r], t1 = a.p.starts[r + 1];
     const int c = tid & 7, g = tid >> 3;  // columns 4c .. 4c+3 of the slice, key rows g + 32 i
     const int hq = h / a.share;
     float *Sp = a.S + ((long long)(a.by_slot ? live : r) * a.heads + h) * (kDK * kDV) + slice * kStepCols + 4 * c;
     const T *qg = static_cast<const T *>(a.q), *kg = static_cast<const T *>(a.k), *vg = static_cast<const T *>(a.v);
     float S[4][4];
-    const bool fresh = a.p.fresh[r] != 0;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!fresh) x = *reinterpret_cast<const float4 *>(Sp + (g + 32 * i) * kDV);
+        if (!fresh) x = __ldcs(reinterpret_cast<const float4 *>(Sp + (g + 32 * i) * kDV));
         S[i][0] = x.x; S[i][1] = x.y; S[i][2] = x.z; S[i][3] = x.w;
     }
     // threads 0..127 fetch k (and alpha), 128..255 q, and 32 of them v
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kStepThreads) k_prompt_steps(PromptArgs a)
     }
 #pragma unroll
     for (int i = 0; i < 4; i++)
-        *reinterpret_cast<float4 *>(Sp + (g + 32 * i) * kDV) = make_float4(S[i][0], S[i][1], S[i][2], S[i][3]);
+        __stcs(reinterpret_cast<float4 *>(Sp + (g + 32 * i) * kDV), make_float4(S[i][0], S[i][1], S[i][2], S[i][3]));
 }
 
 template <class T>

@@ -149,6 +149,9 @@ __device__ __forceinline__ __half to_t<__half>(float x) { return __float2half_rn
 template <>
 __device__ __forceinline__ __nv_bfloat16 to_t<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+constexpr int kOrdered = 256;  // requests of a batch up to which they are ordered (more fill the GPU evenly)
+static_assert(kOrdered <= kWalkThreads, "a request a thread");
+
 template <class T, int V, int NP>
 __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, int first_block, int n_blocks, Scratch sc)
 {
@@ -157,7 +160,24 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
     extern __shared__ __align__(1024) char smem[];
     volatile int *s_dead = reinterpret_cast<volatile int *>(smem + W::oFlags + 4);
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
-    const int r = blockIdx.x / a.heads, h = blockIdx.x - r * a.heads;
+    int r = blockIdx.x / a.heads;
+    const int h = blockIdx.x - r * a.heads;
+    if (a.p.requests <= kOrdered) {
+        // the requests with the most blocks go first: of a batch that fills the
+        // GPU a few times over, a long one at the end would be waited for alone
+        int *n = reinterpret_cast<int *>(smem), *at = n + kOrdered;
+        if (tid < a.p.requests) n[tid] = a.p.block_starts[tid + 1] - a.p.block_starts[tid];
+        __syncthreads();
+        if (tid < a.p.requests) {
+            const int mine = n[tid];
+            int rank = 0;
+            for (int i = 0; i < a.p.requests; i++) rank += n[i] > mine || (n[i] == mine && i < tid);
+            if (rank == r) *at = tid;
+        }
+        __syncthreads();
+        r = *at;
+        __syncthreads();
+    }
     const int live = a.p.live[r];
     if (live < 0) return;
     // the request's blocks of this launch
@@ -505,7 +525,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
 }
 
 // Blocks of a launch: the scratch stays near this size however long the batch is.
-constexpr size_t kScratchTarget = (size_t)256 << 20;
+constexpr size_t kScratchTarget = (size_t)1 << 30;
 
 int launch_blocks(const PromptArgs &a)
 {
