@@ -41,7 +41,7 @@ constexpr int kStepThreads = 256;
 constexpr int kStepSlices = kDV / kStepCols;
 
 template <class T, int V>
-__global__ void __launch_bounds__(kStepThreads) k_prompt_steps(PromptArgs a)
+__global__ void __launch_bounds__(kStepThreads, 5) k_prompt_steps(PromptArgs a)
 {
     // three buffers: the one written while token t is processed was last read
     // by token t - 2, which every thread has left at the barrier of t - 1
