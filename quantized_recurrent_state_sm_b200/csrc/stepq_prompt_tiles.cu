@@ -545,19 +545,26 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
 // A gate per key row.  A CTA takes a block and a value head.  The decays differ
 // from row to row, so no product of K and Q alone serves: between blocks of 16
 // tokens the rows are multiplied by what is left of them at the blocks' border
-// (all factors at most 1 for gates at most 1) and then go to the tensor cores,
-// inside 16 tokens the sums run over the multiplied-out decays.  Gates, K and Q
-// are held in fp32, and give their places to the multiplied rows: what is needed
-// of shared memory decides how many CTAs lie side by side (two).
+// (all factors at most 1 for gates at most 1) and then go to the tensor cores.
+// Inside 16 tokens they do so, too, with the border in the middle and quotients
+// for the rows on its wrong side, as long as no product of eight gates is below
+// kNear; a block of 16 that forgets faster takes the sums over the multiplied-out
+// decays.  Gates, K and Q are held in fp32, and give their places to the
+// multiplied rows: what is needed of shared memory decides how many CTAs lie side
+// by side (two).
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 constexpr int kRowLd = kDK + 4;  // row of a [64][128] fp32 matrix
+// Rows grow by at most 1 / kNear against their scale, of which kRoom is kept
+// free: halves then still hold 28 bits below the row's largest value.
+constexpr float kNear = 1.f / 4096, kRoom = 1.f / 1024;
 struct GateRows {
     __align__(128) float a[kC][kRowLd], k[kC][kRowLd], q[kC][kRowLd];  // gates, K, Q; then K times what is left, K and Q times what was kept
-    float diag_a[4][16][17], diag_p[4][16][17];  // A and P inside 16 tokens
-    float blk[4][kDK];                           // products of 16 tokens' gates
+    float diag_a[4][16][16], diag_p[4][16][16];  // A and P inside 16 tokens that forget fast
+    float blk[4][kDK], mid[4][kDK];              // products of 16 tokens' gates, and of their first eight
     float ek[kC], eq[kC], ek2[kC], beta[kC];
-    float ks[kC], kb[kC], qs[kC], qb[kC];        // scale and unscale of the rows of K and Q
+    float ks[kC], qs[kC];                        // scales of the rows of K and Q
+    int fast[4];                                 // 16 tokens without a product of eight gates below kNear
 };
 static_assert(sizeof(GateRows) <= 115712 && sizeof(Squares) <= sizeof(GateRows::a) + sizeof(GateRows::k), "two CTAs of an SM; room for the squares");
 
@@ -593,28 +600,37 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
                 y[i] = load4(qg + row * a.stride_q);
             }
         }
+        if (tid < 4) r.fast[tid] = 1;
         if (tid < kC) r.beta[tid] = tid < k.n ? a.beta[(long long)(k.t0 + tid) * a.heads + h] : 0.f;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int row = 8 * w + i;
             *reinterpret_cast<float4 *>(&r.k[row][4 * l]) = x[i];
             *reinterpret_cast<float4 *>(&r.q[row][4 * l]) = y[i];
-            float s, b, s2, b2;
-            dev::row_scale(warp_max(x[i]), &s, &b);
-            dev::row_scale(warp_max(y[i]), &s2, &b2);
+            float sk, sq, back;
+            dev::row_scale(warp_max(x[i]), &sk, &back);
+            dev::row_scale(warp_max(y[i]), &sq, &back);
             if (l == 0) {
-                r.ks[row] = s; r.kb[row] = b;
-                r.qs[row] = s2; r.qb[row] = b2;
+                r.ks[row] = sk;
+                r.qs[row] = sq;
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncthreads();
-    // inside 16 tokens: a warp takes four columns s at a time, four key rows a
-    // lane, and walks down the rows t; two turns of four columns, a long and a
-    // short one
+    for (int x = tid; x < 8 * kDK; x += kGateThreads) {  // eight tokens of a key row
+        float p = 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) p *= r.a[x / kDK * 8 + i][x % kDK];
+        if (!(p >= kNear)) r.fast[x / kDK / 2] = 0;
+    }
+    __syncthreads();
+    // inside 16 tokens that forget fast: a warp takes four columns s at a time,
+    // four key rows a lane, and walks down the rows t; two turns of four columns,
+    // a long and a short one
 #pragma unroll 1
     for (int turn = 0; turn < 2; turn++) {
+        if (r.fast[w >> 1]) break;
         const int b = w >> 1, i0 = (w & 1) ? 4 + 4 * turn : 12 * turn, first = 16 * b;
         float2 x[4][2];
 #pragma unroll
@@ -678,6 +694,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
             al[i] = r.a[16 * b + i][d];
             kk[i] = r.k[16 * b + i][d];
             p *= al[i];
+            if (i == 7) r.mid[b][d] = p;
             r.k[16 * b + i][d] = kk[i] * p;
             r.q[16 * b + i][d] *= p;
         }
@@ -712,63 +729,89 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
             }
         }
     }
-    // rows of 16 tokens m against those of the earlier 16s, K by warps 0-3, Q by 4-7
+    // rows of 16 tokens m against those of the earlier 16s and their own, K by
+    // warps 0-3, Q by 4-7
     const int m = w & 3;
-    const bool is_q = w >= 4;
+    const bool is_q = w >= 4, fast = r.fast[m] != 0;
     float acc[kC / 8][4] = {};
     {
         const float(*src)[kRowLd] = is_q ? r.q : r.k;
         const int r0 = 16 * m + g, r1 = r0 + 8;
         const float s0 = (is_q ? r.qs : r.ks)[r0], s1 = (is_q ? r.qs : r.ks)[r1];
+        auto times = [](float2 x, float2 f) { return make_float2(x.x * f.x, x.y * f.y); };
         auto pair = [&](const float *row, int col, float scale) {
             const float2 u = *reinterpret_cast<const float2 *>(row + col);
             return make_float2(u.x * scale, u.y * scale);
         };
+        float own[2][4] = {};
 #pragma unroll 1
         for (int ks = 0; ks < kDK / 16; ks++) {
-            if (m == 0) break;
-            uint32_t ah[4], al[4];
-            float2 between[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+            float2 left[2][2];  // of rows g, g + 8: columns 2 c.., 2 c + 8..
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const int col = 16 * ks + 8 * e + 2 * c;
-                dev::split_half(pair(src[r0], col, s0), &ah[2 * e], &al[2 * e]);
-                dev::split_half(pair(src[r1], col, s1), &ah[2 * e + 1], &al[2 * e + 1]);
+                left[0][e] = pair(src[r0], col, s0);
+                left[1][e] = pair(src[r1], col, s1);
             }
-#pragma unroll
-            for (int j = 2; j >= 0; j--) {
-                if (j >= m) continue;
-                uint32_t bh_[2][2], bl[2][2];
+            // rows of 16 tokens j, times f, as the right operand of a product with x
+            auto product = [&](float (*out)[4], const float2 (*x)[2], int j, const float2 *f, float scale) {
+                uint32_t ah[4], al[4], bh_[2][2], bl[2][2];
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const int col = 16 * ks + 8 * e + 2 * c;
-                    if (j + 1 < m) {  // another 16 tokens between
-                        const float2 f = *reinterpret_cast<const float2 *>(&r.blk[j + 1][col]);
-                        between[e].x *= f.x;
-                        between[e].y *= f.y;
-                    }
-                    const float2 x = pair(r.a[16 * j + g], col, r.ks[16 * j + g]), y = pair(r.a[16 * j + g + 8], col, r.ks[16 * j + g + 8]);
-                    dev::split_half(x.x * between[e].x, x.y * between[e].y, &bh_[0][e], &bl[0][e]);
-                    dev::split_half(y.x * between[e].x, y.y * between[e].y, &bh_[1][e], &bl[1][e]);
+                    dev::split_half(x[0][e], &ah[2 * e], &al[2 * e]);
+                    dev::split_half(x[1][e], &ah[2 * e + 1], &al[2 * e + 1]);
+                    dev::split_half(times(pair(r.a[16 * j + g], col, r.ks[16 * j + g] * scale), f[e]), &bh_[0][e], &bl[0][e]);
+                    dev::split_half(times(pair(r.a[16 * j + g + 8], col, r.ks[16 * j + g + 8] * scale), f[e]), &bh_[1][e], &bl[1][e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 2; e++) mma16816(acc[2 * j + e], al[0], al[1], al[2], al[3], bh_[e][0], bh_[e][1]);
+                for (int e = 0; e < 2; e++) mma16816(out[e], al[0], al[1], al[2], al[3], bh_[e][0], bh_[e][1]);
 #pragma unroll
-                for (int e = 0; e < 2; e++) mma16816(acc[2 * j + e], ah[0], ah[1], ah[2], ah[3], bl[e][0], bl[e][1]);
+                for (int e = 0; e < 2; e++) mma16816(out[e], ah[0], ah[1], ah[2], ah[3], bl[e][0], bl[e][1]);
 #pragma unroll
-                for (int e = 0; e < 2; e++) mma16816(acc[2 * j + e], ah[0], ah[1], ah[2], ah[3], bh_[e][0], bh_[e][1]);
+                for (int e = 0; e < 2; e++) mma16816(out[e], ah[0], ah[1], ah[2], ah[3], bh_[e][0], bh_[e][1]);
+            };
+            if (fast) {
+                float2 x[2][2], f[2];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int col = 16 * ks + 8 * e + 2 * c;
+                    const float2 mid = *reinterpret_cast<const float2 *>(&r.mid[m][col]), all = *reinterpret_cast<const float2 *>(&r.blk[m][col]);
+                    const float2 inv = make_float2(kRoom / mid.x, kRoom / mid.y);
+                    x[0][e] = times(left[0][e], inv);
+                    x[1][e] = times(left[1][e], inv);
+                    f[e] = make_float2(mid.x / all.x, mid.y / all.y);
+                }
+                product(own, x, m, f, kRoom);
+            }
+            float2 between[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+#pragma unroll
+            for (int j = 2; j >= 0; j--) {
+                if (j >= m) continue;
+                if (j + 1 < m)  // another 16 tokens between
+#pragma unroll
+                    for (int e = 0; e < 2; e++) between[e] = times(between[e], *reinterpret_cast<const float2 *>(&r.blk[j + 1][16 * ks + 8 * e + 2 * c]));
+                product(&acc[2 * j], left, j, between, 1.f);
             }
         }
-        const float f0 = is_q ? r.qb[r0] : r.kb[r0] * r.beta[r0], f1 = is_q ? r.qb[r1] : r.kb[r1] * r.beta[r1];
-        const float(*diag)[17] = is_q ? r.diag_p[m] : r.diag_a[m];
+        // unscales: exact quotients of powers of two
+        const float f0 = (is_q ? 1.f : r.beta[r0]) / s0, f1 = (is_q ? 1.f : r.beta[r1]) / s1;
+        const float(*diag)[16] = is_q ? r.diag_p[m] : r.diag_a[m];
 #pragma unroll
         for (int j = 0; j < kC / 8; j++) {
-            const int s = 8 * j + 2 * c;
+            const int i = 8 * (j & 1) + 2 * c, d = is_q ? 0 : 1;  // P has its diagonal, A does not
+            const float2 sb = *reinterpret_cast<const float2 *>(&r.ks[8 * j + 2 * c]);
+            const float2 kb = make_float2(1.f / sb.x, 1.f / sb.y);
             if (j < 2 * m) {
-                const float2 kb = *reinterpret_cast<const float2 *>(&r.kb[s]);
                 acc[j][0] *= f0 * kb.x; acc[j][1] *= f0 * kb.y; acc[j][2] *= f1 * kb.x; acc[j][3] *= f1 * kb.y;
+            } else if (j < 2 * m + 2 && fast) {
+                const float *x = own[j & 1];
+                const float big = 1.f / (kRoom * kRoom);
+                acc[j][0] = i + d <= g ? x[0] * (f0 * kb.x) * big : 0.f;
+                acc[j][1] = i + 1 + d <= g ? x[1] * (f0 * kb.y) * big : 0.f;
+                acc[j][2] = i + d <= g + 8 ? x[2] * (f1 * kb.x) * big : 0.f;
+                acc[j][3] = i + 1 + d <= g + 8 ? x[3] * (f1 * kb.y) * big : 0.f;
             } else if (j < 2 * m + 2) {
-                const int i = s & 15;
                 acc[j][0] = diag[g][i]; acc[j][1] = diag[g][i + 1]; acc[j][2] = diag[g + 8][i]; acc[j][3] = diag[g + 8][i + 1];
             }
         }

@@ -315,11 +315,13 @@ def test_prompt_long(G, variant, dtype):
 @pytest.mark.gpu
 @pytest.mark.parametrize("variant", [GDN, KDA, LINEAR])
 @pytest.mark.parametrize("max_length", [8, None])
-@pytest.mark.parametrize("kind", ["open", "shut", "tiny", "mixed", "nobeta", "onebeta", "zero", "small", "large"])
+@pytest.mark.parametrize("kind", ["open", "quick", "quicker", "shut", "tiny", "mixed", "nobeta", "onebeta", "zero", "small", "large"])
 def test_prompt_extreme_gates_and_scales(G, variant, max_length, kind):
     def change(q, k, v, alpha, beta, St):
         if kind == "open":
             alpha = torch.ones_like(alpha)
+        elif kind in ("quick", "quicker"):  # about where eight gates' product passes 2^-12
+            alpha = 0.2 * (alpha - 0.75) + (0.42 if kind == "quick" else 0.355)
         elif kind == "shut":  # a gate of 0 forgets everything
             alpha = torch.where(torch.arange(len(alpha), device="cuda").reshape(-1, *[1] * (alpha.dim() - 1)) % 3 == 1, 0.0, alpha)
         elif kind == "tiny":
