@@ -72,9 +72,13 @@ __device__ __forceinline__ uint32_t pack_half(float x, float y)
 __device__ __forceinline__ void split_half(float2 x, uint32_t *hi, uint32_t *lo)
 {
     const __half2 h = __float22half2_rn(x);
-    const float2 d = __ffma2_rn(__half22float2(h), make_float2(-1.f, -1.f), x);
     *hi = *reinterpret_cast<const uint32_t *>(&h);
-    *lo = pack_half(d.x, d.y);
+    float a, b;  // x - h, exact (0xbc00 is -1)
+    asm("{\n\t.reg .b16 l, u, m;\n\tmov.b32 {l, u}, %2;\n\tmov.b16 m, 0xbc00;\n\t"
+        "fma.rn.f32.f16 %0, l, m, %3;\n\tfma.rn.f32.f16 %1, u, m, %4;\n\t}"
+        : "=f"(a), "=f"(b)
+        : "r"(*hi), "f"(x.x), "f"(x.y));
+    *lo = pack_half(a, b);
 }
 __device__ __forceinline__ void split_half(float x, float y, uint32_t *hi, uint32_t *lo) { split_half(make_float2(x, y), hi, lo); }
 

@@ -222,12 +222,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
     if (w == kValueWarp) {
         // ---- V: rows of the request's tokens, as 16-byte copies of all lanes (a bulk copy a row would cost its issue, 64 times) ----
         const T *vg = static_cast<const T *>(a.v) + h * kDV;
-        constexpr int pieces = W::kVRow / 16;
-        for (int it = 0; it < count; it++) {
-            const int t0 = row0 + it * kC, n = min(kC, row_end - t0);
+        constexpr int pieces = W::kVRow / 16, rows = 32 / pieces;  // rows at a time: two of 16-bit, one of 32-bit elements
+        const T *src = vg + (long long)(row0 + l / pieces) * a.stride_v + l % pieces * (16 / (int)sizeof(T));
+        char *dst = smem + W::oV + l / pieces * W::kVRow + l % pieces * 16;
+        for (int it = 0; it < count; it++, src += kC * a.stride_v) {
+            const int n = min(kC, row_end - row0 - it * kC);
             if (it > 0) wait(V == kLinear ? kGotU : kGotR, (it - 1) & 1);  // the rows before are read
-            for (int i = l; i < n * pieces; i += 32)
-                cp_async16(smem + W::oV + i / pieces * W::kVRow + i % pieces * 16, vg + (long long)(t0 + i / pieces) * a.stride_v + i % pieces * (16 / (int)sizeof(T)));
+            const T *p = src;
+#pragma unroll 8
+            for (int i = 0; i < kC / rows; i++, p += rows * a.stride_v)
+                if (i * rows + l / pieces < n) cp_async16(dst + i * rows * W::kVRow, p);
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(dev::smem_addr(&bar[kFullV])) : "memory");
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -390,9 +394,19 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
                 for (int t = 0; t < 8; t++) {
                     const float2 fq = __fmul2_rn(pair_at(ov + t1 + 2 * t), make_float2(sb, sb)), fp = __fmul2_rn(pair_at(ov + kC + t1 + 2 * t), make_float2(rb, rb));
                     o[t] = __ffma2_rn(p[t], fp, __fmul2_rn(o[t], fq));
-                    if (t1 + 2 * t < n) dst[0] = to_t<T>(o[t].x);
-                    if (t1 + 2 * t + 1 < n) dst[row] = to_t<T>(o[t].y);
-                    dst += 2 * row;
+                }
+                if (n == kC) {
+#pragma unroll
+                    for (int t = 0; t < 8; t++, dst += 2 * row) {
+                        dst[0] = to_t<T>(o[t].x);
+                        dst[row] = to_t<T>(o[t].y);
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 8; t++, dst += 2 * row) {
+                        if (t1 + 2 * t < n) dst[0] = to_t<T>(o[t].x);
+                        if (t1 + 2 * t + 1 < n) dst[row] = to_t<T>(o[t].y);
+                    }
                 }
             }
             tc::fence_before();

@@ -2,7 +2,6 @@
 // packing by request, beam selection and reordering.  Argument validation and
 // launches; no device allocation.
 #include <climits>
-#include <string>
 
 #include "stepq_host.cuh"
 #include "stepq_serve.cuh"
@@ -197,13 +196,12 @@ stepq_status stepq_plan_check(const stepq_plan_desc *desc, const void *plan, siz
     if (bits == 0) return STEPQ_OK;
     if (bits & STEPQ_PLAN_TIMEOUT)
         return fail(STEPQ_ERR_CUDA, "a prompt kernel gave up waiting for a copy; its requests' states and rows are not valid");
-    std::string why;
-    if (bits & STEPQ_PLAN_BAD_LENGTH) why += "; a length below 0 or above max_length";
-    if (bits & STEPQ_PLAN_TOO_MANY) why += "; more tokens than the plan's capacity";
-    if (bits & STEPQ_PLAN_BAD_SLOT) why += "; a slot out of range, or none given";
-    if (bits & STEPQ_PLAN_SLOT_TWICE) why += "; two requests in one slot";
-    if (bits & STEPQ_PLAN_NO_SLOT) why += "; no free slot left";
-    return fail(STEPQ_ERR_INVALID_ARG, "the plan refused requests%s", why.c_str());
+    return fail(STEPQ_ERR_INVALID_ARG, "the plan refused requests%s%s%s%s%s",
+                bits & STEPQ_PLAN_BAD_LENGTH ? "; a length below 0 or above max_length" : "",
+                bits & STEPQ_PLAN_TOO_MANY ? "; more tokens than the plan's capacity" : "",
+                bits & STEPQ_PLAN_BAD_SLOT ? "; a slot out of range, or none given" : "",
+                bits & STEPQ_PLAN_SLOT_TWICE ? "; two requests in one slot" : "",
+                bits & STEPQ_PLAN_NO_SLOT ? "; no free slot left" : "");
 }
 
 size_t stepq_prompt_scratch_bytes(const stepq_plan_desc *plan_desc, const stepq_prompt_desc *desc)
