@@ -265,7 +265,12 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_block_walk(PromptArgs a, in
         if (V != kLinear) copy(kFullInv, W::oInv, sc.inv + bh(0) * kSquareBytes, kSquareBytes);
         copy(kFullP, W::oP, sc.p + bh(0) * kSquareBytes, kSquareBytes);
         const uint32_t base = dev::smem_addr(smem);
-        // products of S^T with the rows of an operand tile
+        // Products that share a right operand follow one another: in an order by
+        // halves instead (low ones first, while the sums, which are cut off at
+        // every product, are small) the operand is fetched anew each time, and a
+        // block took 7.9 thousand cycles instead of 7.2, for an error of fp32
+        // prompts of 5.2e-7 instead of 7e-7.
+        // products of S^T with the rows of an operand tile, the even or odd 16s of key rows
         auto with_rows = [&](uint32_t d, uint32_t rows, int odd) {
             bool add = odd != 0;
 #pragma unroll

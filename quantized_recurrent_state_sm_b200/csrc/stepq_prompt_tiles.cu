@@ -408,6 +408,7 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
 {
     extern __shared__ __align__(128) char smem[];
     __shared__ float ek[kC], eq[kC], s_beta[kC], s_pre[kC], s_suf[kC], s_blk[4], s_diag[4][16][17];
+    __shared__ double s_keep[2];
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3;
     Block k;
     const int h = blockIdx.x % a.heads, hq = h / a.share;
@@ -438,6 +439,12 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
             if ((l & 15) >= d) p *= x;
             if ((l & 15) + d < 16) q *= y;
         }
+        // what a block keeps of the state is multiplied up block after block: its
+        // product is rounded once
+        double all = (double)alpha;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) all *= __shfl_xor_sync(kFull, all, d);
+        if (l == 0) s_keep[w] = all;
         s_pre[tid] = p;
         s_suf[tid] = q;
         s_beta[tid] = beta;
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
         sv[tid] = -s_beta[tid] * ct * ek[tid];
         sv[kC + tid] = s_beta[tid];
         sv[2 * kC + tid] = V == kLinear ? left : sq.t_back[tid] * left;
-        if (tid == kC - 1) sv[3 * kC] = ct;
+        if (tid == 0) sv[3 * kC] = (float)(s_keep[0] * s_keep[1]);
         ov[tid] = ct * eq[tid];
         ov[kC + tid] = sq.p_back[tid];
     }
@@ -681,6 +688,13 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
             for (int u = 0; u < 4; u++) r.diag_a[b][l][i0 + u] = r.diag_p[b][l][i0 + u] = 0.f;
         }
     }
+    __syncthreads();
+    // what a block keeps of a key row is multiplied up block after block: its
+    // product is rounded once
+    double keep = 1.0;
+    if (tid >= kDK)
+#pragma unroll 8
+        for (int i = 0; i < kC; i++) keep *= (double)r.a[i][tid - kDK];
     __syncthreads();
     // gates of 16 tokens of a key row: what is kept from the 16's start, and what
     // is left at its end
@@ -830,8 +844,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
         ov[tid] = r.eq[tid];
         ov[kC + tid] = sq.p_back[tid];
     } else if (tid >= kDK) {
-        const int d = tid - kDK;
-        sv[3 * kC + d] = r.blk[0][d] * r.blk[1][d] * r.blk[2][d] * r.blk[3][d];
+        sv[3 * kC + tid - kDK] = (float)keep;
     }
     if (tid == 0) bulk_wait();
 }
