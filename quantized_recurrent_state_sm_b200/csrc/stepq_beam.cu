@@ -98,10 +98,10 @@ struct RowStats {
 // ---------------------------------------------------------------------------
 // One pass over the logits.  A CTA takes every `splits`-th tile of a row into
 // registers (PER values a thread), sums the exponentials under a running
-// maximum, and keeps the n best keys: the n-th largest of the 256 threads'
-// maxima bounds the n-th best of the tile from below, so only the few values
-// above it are collected and ranked.  At most n threads hold such values, which
-// bounds the list.  Bound by reading the logits.
+// maximum, and keeps the n best keys: the worst of those kept so far, and the
+// n-th largest of the 256 threads' maxima, bound the n-th best from below, so
+// only the few values above are collected and ranked.  At most n threads hold
+// such values, which bounds the list.
 // ---------------------------------------------------------------------------
 template <class T, int PER>
 __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int splits, RowStats *stats,
@@ -163,14 +163,19 @@ __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int spli
             sum = sum * (top == m ? 1.0 : (double)expf(top - m)) + (double)part_sum;
             top = m;
         }
-        // threshold: the n-th largest of the threads' maxima (1 if fewer are there)
-        int rank = 0;
-        for (int i = 0; i < kScanThreads; i++) rank += s_max[i] > mine;
-        if (mine && rank == a.n - 1) s_tau = mine;
-        __syncthreads();
-        unsigned long long tau = s_tau;
-        if (kept == a.n && s_keep[a.n - 1] > tau) tau = s_keep[a.n - 1] + 1;
+        // threshold: the worst of the n kept, and where that leaves more than n
+        // threads with candidates the n-th largest of the threads' maxima, too
+        const unsigned long long floor_key = kept == a.n ? s_keep[a.n - 1] : 0;
+        const int above = __syncthreads_count(mine > floor_key);
+        if (above == 0) continue;  // the tile adds nothing
+        if (above > a.n) {
+            int rank = 0;
+            for (int i = 0; i < kScanThreads; i++) rank += s_max[i] > mine;
+            if (rank == a.n - 1) s_tau = mine;
+        }
         if (tid < kept) s_list[tid] = s_keep[tid];
+        __syncthreads();
+        const unsigned long long tau = s_tau > floor_key ? s_tau : floor_key + 1;
         if (mine >= tau) {
 #pragma unroll
             for (int i = 0; i < PER; i++) {
@@ -226,16 +231,23 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(BeamArgs a, int sp
     __shared__ int s_count;
     const int tid = threadIdx.x, g = blockIdx.x, B = a.beams, n = a.n;
     const Cand none = {-INFINITY, 0x7fffffff, 0x7fffffff};
-    if (tid < B) {
-        const RowStats *st = stats + (long long)(g * B + tid) * splits;
+    // a warp a beam and turn, a lane a part: one wait for all of a beam's statistics
+    for (int b = tid >> 5; b < B; b += kMergeThreads / 32) {
+        const RowStats *st = stats + (long long)(g * B + b) * splits;
         float top = -INFINITY;
-        for (int i = 0; i < splits; i++) top = fmaxf(top, st[i].top);
+        for (int i = tid & 31; i < splits; i += 32) top = fmaxf(top, st[i].top);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
         double sum = 0.0;
-        for (int i = 0; i < splits; i++)
+        for (int i = tid & 31; i < splits; i += 32)
             if (st[i].top > -INFINITY) sum += st[i].sum * (st[i].top == top ? 1.0 : exp((double)st[i].top - (double)top));
-        const float s = a.scores[(long long)g * B + tid];
-        s_top[tid] = top;
-        s_add[tid] = sum > 0.0 && s > -INFINITY ? (double)s - log(sum) : -INFINITY;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+        if ((tid & 31) == 0) {
+            const float s = a.scores[(long long)g * B + b];
+            s_top[b] = top;
+            s_add[b] = sum > 0.0 && s > -INFINITY ? (double)s - log(sum) : -INFINITY;
+        }
     }
     if (tid == 0) { s_tau = none; s_count = 0; }
     __syncthreads();
@@ -257,7 +269,8 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(BeamArgs a, int sp
     s_best[tid] = mine;
     __syncthreads();
     int rank = 0;
-    for (int i = 0; i < kMergeThreads; i++) rank += better(s_best[i], mine);
+    const int holders = min(kMergeThreads, total);  // threads that saw a candidate
+    for (int i = 0; i < holders; i++) rank += better(s_best[i], mine);
     if (mine.score > -INFINITY && rank == n - 1) s_tau = mine;
     __syncthreads();
     const Cand tau = s_tau;
