@@ -98,21 +98,26 @@ struct RowStats {
 // ---------------------------------------------------------------------------
 // One pass over the logits.  A CTA takes every `splits`-th tile of a row into
 // registers (PER values a thread), sums the exponentials under a running
-// maximum, and keeps the n best keys: the worst of those kept so far, and the
-// n-th largest of the 256 threads' maxima, bound the n-th best from below, so
-// only the few values above are collected and ranked.  At most n threads hold
-// such values, which bounds the list.
+// maximum, and keeps the n best keys.  The worst of those kept so far bounds the
+// n-th best from below, so a later tile mostly adds few values or none.  Where
+// more than n threads are above that, the n-th largest of the maxima of 64 groups
+// of four threads is a first bound, and the n-th largest of the few threads'
+// maxima that reach it the second: at most n threads hold values above, which
+// bounds the list that is ranked.
 // ---------------------------------------------------------------------------
+constexpr int kGroups = kScanThreads / 4;
+static_assert(kGroups >= kMaxBeams, "as many groups as values can be kept");
+
 template <class T, int PER>
 __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int splits, RowStats *stats,
                                                             unsigned long long *best)
 {
     constexpr int E = 16 / sizeof(T), NV = PER / E;
-    __shared__ unsigned long long s_max[kScanThreads], s_list[kMaxBeams * PER + kMaxBeams], s_keep[kMaxBeams];
+    __shared__ unsigned long long s_group[kGroups], s_near[kScanThreads], s_list[kMaxBeams * PER + kMaxBeams], s_keep[kMaxBeams];
     __shared__ float s_top[kScanThreads / 32];
     __shared__ double s_sum[kScanThreads / 32];
-    __shared__ unsigned long long s_tau;
-    __shared__ int s_count;
+    __shared__ unsigned long long s_low, s_tau;
+    __shared__ int s_count, s_reach;
     const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
     const int row = blockIdx.x / splits, part = blockIdx.x - row * splits;
     const T *x0 = static_cast<const T *>(a.logits) + (long long)row * a.stride;
@@ -125,11 +130,11 @@ __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int spli
     int kept = 0;
     for (int v0 = part * kScanThreads * NV; v0 < n_vec; v0 += splits * kScanThreads * NV) {
         float x[PER];
-        int tok[NV];
+        // token of value i: runs of E tokens, kScanThreads runs apart
+        auto token = [&](int i) { return (v0 + i / E * kScanThreads + tid) * E + i % E; };
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int j = v0 + i * kScanThreads + tid, at = j * E;
-            tok[i] = at;
             // the row's first and last run one by one where their vectors reach past the row
             if (j < n_vec && at + (shift ? 2 * E : E) <= a.vocab && (j > 0 || shift == 0)) {
                 unpack4(load_16(x0 + at, shift), &x[i * E], T{});
@@ -139,39 +144,66 @@ __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int spli
                     x[i * E + e] = (j < n_vec && at + e < a.vocab) ? load_f(x0 + at + e) : -INFINITY;
             }
         }
-        unsigned long long mine = 0;
+        float m = -INFINITY;
 #pragma unroll
         for (int i = 0; i < PER; i++) {
-            if (!(x[i] > -INFINITY)) x[i] = -INFINITY;  // NaN counts as barred
-            const unsigned long long k = key_of(x[i], tok[i / E] + i % E);
-            mine = k > mine ? k : mine;
+            x[i] = fmaxf(x[i], -INFINITY);  // NaN counts as barred
+            m = fmaxf(m, x[i]);
         }
-        s_max[tid] = mine;
-        float m = mine ? value_of(mine) : -INFINITY;
+        // the thread's best: of equal values the first
+        int first = 0;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; i--) first = x[i] == m ? token(i) : first;
+        const unsigned long long mine = key_of(m, first);
+        unsigned long long group = mine;
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+            const unsigned long long other = __shfl_xor_sync(kFull, group, d);
+            group = other > group ? other : group;
+        }
+        if ((l & 3) == 0) s_group[tid >> 2] = group;
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
         if (l == 0) s_top[w] = m;
-        if (tid == 0) { s_tau = 1; s_count = kept; }
+        if (tid == 0) {
+            s_low = s_tau = 1;
+            s_count = kept;
+            s_reach = 0;
+        }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kScanThreads / 32; i++) m = fmaxf(m, s_top[i]);
         m = fmaxf(m, top);
         if (m > -INFINITY) {
+            // the fast exponential is off by up to 2 + 1.2 |x - m| units in the last
+            // place of a term: 1e-6 of the sum where all terms lie 5 below the
+            // maximum, so 1e-6 of a score's unit, which has fp32's 24 bits
             float part_sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < PER; i++) part_sum += x[i] == m ? 1.f : expf(x[i] - m);
+            for (int i = 0; i < PER; i++) part_sum += x[i] == m ? 1.f : __expf(x[i] - m);
             sum = sum * (top == m ? 1.0 : (double)expf(top - m)) + (double)part_sum;
             top = m;
         }
-        // threshold: the worst of the n kept, and where that leaves more than n
-        // threads with candidates the n-th largest of the threads' maxima, too
         const unsigned long long floor_key = kept == a.n ? s_keep[a.n - 1] : 0;
         const int above = __syncthreads_count(mine > floor_key);
         if (above == 0) continue;  // the tile adds nothing
         if (above > a.n) {
             int rank = 0;
-            for (int i = 0; i < kScanThreads; i++) rank += s_max[i] > mine;
-            if (rank == a.n - 1) s_tau = mine;
+#pragma unroll
+            for (int i = 0; i < kGroups / 4; i++) rank += s_group[4 * i + (l & 3)] > group;
+            rank += __shfl_xor_sync(kFull, rank, 1);
+            rank += __shfl_xor_sync(kFull, rank, 2);
+            if ((l & 3) == 0 && group != 0 && rank == a.n - 1) s_low = group;
+            __syncthreads();
+            const bool near = mine > floor_key && mine >= s_low;
+            if (near) s_near[atomicAdd(&s_reach, 1)] = mine;
+            __syncthreads();
+            if (near) {
+                const int reach = s_reach;
+                int before = 0;
+                for (int i = 0; i < reach; i++) before += s_near[i] > mine;
+                if (before == a.n - 1) s_tau = mine;
+            }
         }
         if (tid < kept) s_list[tid] = s_keep[tid];
         __syncthreads();
@@ -179,21 +211,19 @@ __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int spli
         if (mine >= tau) {
 #pragma unroll
             for (int i = 0; i < PER; i++) {
-                const unsigned long long k = key_of(x[i], tok[i / E] + i % E);
+                const unsigned long long k = key_of(x[i], token(i));
                 if (k >= tau) s_list[atomicAdd(&s_count, 1)] = k;
             }
         }
         __syncthreads();
         const int count = s_count;
-        if (count > kept) {  // otherwise the tile adds nothing
-            for (int i = tid; i < count; i += kScanThreads) {
-                const unsigned long long k = s_list[i];
-                int above = 0;
-                for (int j = 0; j < count; j++) above += s_list[j] > k;
-                if (above < a.n) s_keep[above] = k;
-            }
-            kept = min(count, a.n);
+        for (int i = tid; i < count; i += kScanThreads) {
+            const unsigned long long k = s_list[i];
+            int better = 0;
+            for (int j = 0; j < count; j++) better += s_list[j] > k;
+            if (better < a.n) s_keep[better] = k;
         }
+        kept = min(count, a.n);
         __syncthreads();
     }
 #pragma unroll
@@ -215,8 +245,9 @@ struct Cand {
 
 __device__ __forceinline__ bool better(const Cand &x, const Cand &y)
 {
-    if (x.score != y.score) return x.score > y.score;
-    return x.beam != y.beam ? x.beam < y.beam : x.token < y.token;
+    // without branches; beams and tokens are not negative
+    const unsigned long long at_x = (unsigned long long)(unsigned)x.beam << 32 | (unsigned)x.token, at_y = (unsigned long long)(unsigned)y.beam << 32 | (unsigned)y.token;
+    return (x.score > y.score) | ((x.score == y.score) & (at_x < at_y));
 }
 
 // One CTA a group: the rows' log-sums in fp64, then the n best of all parts'
@@ -270,6 +301,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(BeamArgs a, int sp
     __syncthreads();
     int rank = 0;
     const int holders = min(kMergeThreads, total);  // threads that saw a candidate
+#pragma unroll 8
     for (int i = 0; i < holders; i++) rank += better(s_best[i], mine);
     if (mine.score > -INFINITY && rank == n - 1) s_tau = mine;
     __syncthreads();
