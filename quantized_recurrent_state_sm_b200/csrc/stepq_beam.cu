@@ -87,6 +87,20 @@ __device__ __forceinline__ float4 load_16(const void *p, int shift)
     }
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // What a CTA leaves of its part of a row: the n best, and the softmax
 // statistics (largest logit, sum of exponentials below it).
 struct RowStats {
@@ -144,24 +158,18 @@ __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int spli
                     x[i * E + e] = (j < n_vec && at + e < a.vocab) ? load_f(x0 + at + e) : -INFINITY;
             }
         }
-        float m = -INFINITY;
+        float m = -INFINITY;  // passes over NaN
 #pragma unroll
-        for (int i = 0; i < PER; i++) {
-            x[i] = fmaxf(x[i], -INFINITY);  // NaN counts as barred
-            m = fmaxf(m, x[i]);
+        for (int i = 0; i < PER; i += 2) m = max3(m, x[i], x[i + 1]);
+        // the thread's best, where it may count: of equal values the first
+        const unsigned long long floor_key = kept == a.n ? s_keep[a.n - 1] : 0;
+        unsigned long long mine = 0;
+        if (m > -INFINITY && (floor_key == 0 || m >= value_of(floor_key))) {
+            int first = 0;
+#pragma unroll
+            for (int i = PER - 1; i >= 0; i--) first = x[i] == m ? i : first;
+            mine = key_of(m, token(first));
         }
-        // the thread's best: of equal values the first
-        int first = 0;
-#pragma unroll
-        for (int i = PER - 1; i >= 0; i--) first = x[i] == m ? token(i) : first;
-        const unsigned long long mine = key_of(m, first);
-        unsigned long long group = mine;
-#pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-            const unsigned long long other = __shfl_xor_sync(kFull, group, d);
-            group = other > group ? other : group;
-        }
-        if ((l & 3) == 0) s_group[tid >> 2] = group;
 #pragma unroll
         for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
         if (l == 0) s_top[w] = m;
@@ -175,19 +183,35 @@ __global__ void __launch_bounds__(kScanThreads) k_beam_scan(BeamArgs a, int spli
         for (int i = 0; i < kScanThreads / 32; i++) m = fmaxf(m, s_top[i]);
         m = fmaxf(m, top);
         if (m > -INFINITY) {
-            // the fast exponential is off by up to 2 + 1.2 |x - m| units in the last
-            // place of a term: 1e-6 of the sum where all terms lie 5 below the
-            // maximum, so 1e-6 of a score's unit, which has fp32's 24 bits
-            float part_sum = 0.f;
+            // a term e^-d is off by 2^-23 (2 + d) of itself: 1e-6 of the sum if all
+            // lie 5 below the maximum, and so 1e-6 of a unit of the score
+            float2 terms = make_float2(0.f, 0.f);
+            const float2 off = make_float2(-m, -m), base = make_float2(1.44269504f, 1.44269504f);
 #pragma unroll
-            for (int i = 0; i < PER; i++) part_sum += x[i] == m ? 1.f : __expf(x[i] - m);
+            for (int i = 0; i < PER; i += 2) {
+                const float2 d = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), off), base);
+                terms = __fadd2_rn(terms, make_float2(exp2_fast(d.x), exp2_fast(d.y)));
+            }
+            float part_sum = terms.x + terms.y;
+            if (part_sum != part_sum) {  // NaN counts as barred; a value of +inf is the maximum
+                part_sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < PER; i++) part_sum += x[i] == m ? 1.f : (x[i] < m ? expf(x[i] - m) : 0.f);
+            }
             sum = sum * (top == m ? 1.0 : (double)expf(top - m)) + (double)part_sum;
             top = m;
         }
-        const unsigned long long floor_key = kept == a.n ? s_keep[a.n - 1] : 0;
         const int above = __syncthreads_count(mine > floor_key);
         if (above == 0) continue;  // the tile adds nothing
         if (above > a.n) {
+            unsigned long long group = mine;
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                const unsigned long long other = __shfl_xor_sync(kFull, group, d);
+                group = other > group ? other : group;
+            }
+            if ((l & 3) == 0) s_group[tid >> 2] = group;
+            __syncthreads();
             int rank = 0;
 #pragma unroll
             for (int i = 0; i < kGroups / 4; i++) rank += s_group[4 * i + (l & 3)] > group;
