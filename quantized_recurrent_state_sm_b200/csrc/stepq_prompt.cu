@@ -34,7 +34,13 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // turn.  Columns are independent, so four CTAs share a state.  With p = S'^T k
 // and r = S'^T q summed in the same pass, u = beta (v - p) and out = r + (k.q) u:
 // one exchange between the warps a token.  A single token is bound by the
-// state's bytes (64 KiB in, 64 KiB out a head).
+// state's bytes (64 KiB in, 64 KiB out a head): five CTAs an SM keep enough of
+// them under way, and the states pass the caches (nothing reads them again).
+// Single tokens, gated Delta rule, bf16, 64 requests of 32 heads (270 MB): 53 us,
+// 5.1 TB/s; a gate per key row, fp32, 128 of 32 (547 MB): 105 us, 5.2 TB/s; plain,
+// binary16, 256 of 32 (1.08 GB): 183 us, 5.9 TB/s, of 6.5 that a copy reaches.
+// Every further token costs its chain of loads, shuffles and one barrier: 1.6 us
+// where all CTAs lie on the GPU at once, 45 us a token for 128 requests of 32.
 // ---------------------------------------------------------------------------
 constexpr int kStepCols = 32;
 constexpr int kStepThreads = 256;

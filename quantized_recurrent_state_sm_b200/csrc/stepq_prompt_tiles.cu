@@ -386,6 +386,9 @@ __device__ __forceinline__ bool find_block(const PromptArgs &a, int first_block,
 // token s to token t is the product of what is left of s at the end of its 16
 // tokens, of the 16s between, and of t's 16 up to t; inside 16 tokens it is
 // multiplied out.
+// Measured: bf16, 128 blocks of 32 heads 121 us, 214 MB moved (47 % issue, 14 %
+// of the tensor pipe); fp32, 101 blocks of 32 heads 155 us, where all products
+// are three; plain, binary16, 64 blocks of 32 heads 31 us, without the inverse.
 // ---------------------------------------------------------------------------
 constexpr int kTileThreads = 128;
 
@@ -559,6 +562,9 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
 // decays.  Gates, K and Q are held in fp32, and give their places to the
 // multiplied rows: what is needed of shared memory decides how many CTAs lie side
 // by side (two).
+// Measured: bf16, 101 blocks of 32 heads 343 us, 540 MB moved: 42 % issue (27
+// thousand warp instructions a CTA, half of them making halves), 8 % tensor pipe.
+// With every 16 tokens multiplied out it takes 371 us.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 constexpr int kRowLd = kDK + 4;  // row of a [64][128] fp32 matrix
