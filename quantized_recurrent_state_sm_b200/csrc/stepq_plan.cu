@@ -8,7 +8,7 @@
 // requests that begin in the CTA's range mark their first entry, and a running
 // maximum over the marks finds the last request at or before each entry.
 // Measured: 8 requests 7.5 us (a launch and three rounds to L2), 8192 requests of
-// 660 thousand tokens, half of them taking free slots, 28 us (4 MB written).
+// 454 thousand tokens, half of them taking free slots, 28 us (4 MB written).
 #include "stepq_serve.cuh"
 
 namespace stepq {

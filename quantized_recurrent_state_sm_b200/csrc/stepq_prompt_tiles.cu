@@ -556,28 +556,32 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
 // from row to row, so no product of K and Q alone serves: between blocks of 16
 // tokens the rows are multiplied by what is left of them at the blocks' border
 // (all factors at most 1 for gates at most 1) and then go to the tensor cores.
-// Inside 16 tokens they do so, too, with the border in the middle and quotients
-// for the rows on its wrong side, as long as no product of eight gates is below
-// kNear; a block of 16 that forgets faster takes the sums over the multiplied-out
-// decays.  Gates, K and Q are held in fp32, and give their places to the
-// multiplied rows: what is needed of shared memory decides how many CTAs lie side
-// by side (two).
-// Measured: bf16, 101 blocks of 32 heads 343 us, 540 MB moved: 42 % issue (27
-// thousand warp instructions a CTA, half of them making halves), 8 % tensor pipe.
-// With every 16 tokens multiplied out it takes 371 us.
+// Inside 16 tokens they do so, too, with the border at their end and the left
+// rows divided by the gates behind them, as long as no product of the 16 gates is
+// below kNear; a block of 16 that forgets faster takes the sums over the
+// multiplied-out decays.  All these products share one right operand, K times
+// what is left at the end of its 16, whose halves are made once.  Gates, K and Q
+// are held in fp32, and give their places to the multiplied rows: what is needed
+// of shared memory decides how many CTAs lie side by side (two).
+// Measured: bf16, 105 blocks of 32 heads 298 us, 540 MB moved.  With the right
+// operand's halves made by each warp that reads it 343 us, and with every 16
+// tokens multiplied out 371 us.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 constexpr int kRowLd = kDK + 4;  // row of a [64][128] fp32 matrix
-// Rows grow by at most 1 / kNear against their scale, of which kRoom is kept
-// free: halves then still hold 28 bits below the row's largest value.
-constexpr float kNear = 1.f / 4096, kRoom = 1.f / 1024;
+// Left rows, below 2^14 after scaling, grow by at most 1 / kNear; times kRoom they
+// stay below 2^15.  Values that do not grow then have 2^-2 at most, in halves that
+// resolve 2^-25, and right ones that shrink by 2^-16 the same: 22 bits are kept.
+// Gates of at least a half (half-lives of a token or more) always qualify.
+constexpr float kNear = 1.f / 65536, kRoom = 1.f / 32768;
 struct GateRows {
-    __align__(128) float a[kC][kRowLd], k[kC][kRowLd], q[kC][kRowLd];  // gates, K, Q; then K times what is left, K and Q times what was kept
+    // gates, K, Q; then K times what is left (at last its halves, 256 bytes of each), K and Q times what was kept
+    __align__(128) float a[kC][kRowLd], k[kC][kRowLd], q[kC][kRowLd];
     float diag_a[4][16][16], diag_p[4][16][16];  // A and P inside 16 tokens that forget fast
-    float blk[4][kDK], mid[4][kDK];              // products of 16 tokens' gates, and of their first eight
+    float blk[4][kDK], inv[4][kDK];              // products of 16 tokens' gates, and kRoom by them
     float ek[kC], eq[kC], ek2[kC], beta[kC];
     float ks[kC], qs[kC];                        // scales of the rows of K and Q
-    int fast[4];                                 // 16 tokens without a product of eight gates below kNear
+    int fast[4];                                 // 16 tokens without a product of gates below kNear
 };
 static_assert(sizeof(GateRows) <= 115712 && sizeof(Squares) <= sizeof(GateRows::a) + sizeof(GateRows::k), "two CTAs of an SM; room for the squares");
 
@@ -631,11 +635,11 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncthreads();
-    for (int x = tid; x < 8 * kDK; x += kGateThreads) {  // eight tokens of a key row
+    for (int x = tid; x < 4 * kDK; x += kGateThreads) {  // 16 tokens of a key row
         float p = 1.f;
 #pragma unroll
-        for (int i = 0; i < 8; i++) p *= r.a[x / kDK * 8 + i][x % kDK];
-        if (!(p >= kNear)) r.fast[x / kDK / 2] = 0;
+        for (int i = 0; i < 16; i++) p *= r.a[x / kDK * 16 + i][x % kDK];
+        if (!(p >= kNear)) r.fast[x / kDK] = 0;
     }
     __syncthreads();
     // inside 16 tokens that forget fast: a warp takes four columns s at a time,
@@ -698,9 +702,14 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
     // what a block keeps of a key row is multiplied up block after block: its
     // product is rounded once
     double keep = 1.0;
-    if (tid >= kDK)
-#pragma unroll 8
-        for (int i = 0; i < kC; i++) keep *= (double)r.a[i][tid - kDK];
+    if (tid >= kDK) {
+        double part[4] = {1.0, 1.0, 1.0, 1.0};  // side by side
+#pragma unroll 4
+        for (int i = 0; i < 16; i++)
+#pragma unroll
+            for (int b = 0; b < 4; b++) part[b] *= (double)r.a[16 * b + i][tid - kDK];
+        keep = (part[0] * part[1]) * (part[2] * part[3]);
+    }
     __syncthreads();
     // gates of 16 tokens of a key row: what is kept from the 16's start, and what
     // is left at its end
@@ -714,11 +723,11 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
             al[i] = r.a[16 * b + i][d];
             kk[i] = r.k[16 * b + i][d];
             p *= al[i];
-            if (i == 7) r.mid[b][d] = p;
             r.k[16 * b + i][d] = kk[i] * p;
             r.q[16 * b + i][d] *= p;
         }
         r.blk[b][d] = p;
+        r.inv[b][d] = kRoom / p;  // counts where p is at least kNear
         p = 1.f;
 #pragma unroll
         for (int i = 15; i >= 0; i--) {
@@ -739,9 +748,19 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
 #pragma unroll 4
         for (int i = 0; i < 8; i++) {
             const int row = 8 * w + i;
+            const float4 left = at4(&r.a[row][4 * l]);
             const float b0 = put_row<2, false>(mul4(at4(&r.k[row][4 * l]), before), row, l, img + sc.k),
                         b1 = put_row<2, false>(mul4(at4(&r.q[row][4 * l]), before), row, l, img + sc.q),
-                        b2 = put_row<2, false>(mul4(at4(&r.a[row][4 * l]), behind), row, l, img + sc.k2);
+                        b2 = put_row<2, false>(mul4(left, behind), row, l, img + sc.k2);
+            // the right operand's halves, in the row's own place
+            const float scale = r.ks[row];
+            uint32_t hi[2], lo[2];
+            dev::split_half(left.x * scale, left.y * scale, &hi[0], &lo[0]);
+            dev::split_half(left.z * scale, left.w * scale, &hi[1], &lo[1]);
+            __syncwarp();
+            char *at = reinterpret_cast<char *>(r.a[row]) + 8 * l;
+            *reinterpret_cast<uint2 *>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(at + 2 * kDK) = make_uint2(lo[0], lo[1]);
             if (l == 0) {
                 r.ek[row] = b0;
                 r.eq[row] = b1;
@@ -749,6 +768,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
             }
         }
     }
+    __syncthreads();
     // rows of 16 tokens m against those of the earlier 16s and their own, K by
     // warps 0-3, Q by 4-7
     const int m = w & 3;
@@ -758,31 +778,28 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
         const float(*src)[kRowLd] = is_q ? r.q : r.k;
         const int r0 = 16 * m + g, r1 = r0 + 8;
         const float s0 = (is_q ? r.qs : r.ks)[r0], s1 = (is_q ? r.qs : r.ks)[r1];
-        auto times = [](float2 x, float2 f) { return make_float2(x.x * f.x, x.y * f.y); };
-        auto pair = [&](const float *row, int col, float scale) {
-            const float2 u = *reinterpret_cast<const float2 *>(row + col);
-            return make_float2(u.x * scale, u.y * scale);
-        };
+        const uint32_t right = dev::smem_addr(r.a[(l & 7) + (l >> 4) * 8]) + ((l >> 3) & 1) * 16;
+        auto pair = [&](const float *row, int col) { return *reinterpret_cast<const float2 *>(row + col); };
         float own[2][4] = {};
-#pragma unroll 1
+#pragma unroll 2
         for (int ks = 0; ks < kDK / 16; ks++) {
+            const int col = 16 * ks + 2 * c;
             float2 left[2][2];  // of rows g, g + 8: columns 2 c.., 2 c + 8..
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const int col = 16 * ks + 8 * e + 2 * c;
-                left[0][e] = pair(src[r0], col, s0);
-                left[1][e] = pair(src[r1], col, s1);
+                left[0][e] = __fmul2_rn(pair(src[r0], col + 8 * e), make_float2(s0, s0));
+                left[1][e] = __fmul2_rn(pair(src[r1], col + 8 * e), make_float2(s1, s1));
             }
-            // rows of 16 tokens j, times f, as the right operand of a product with x
-            auto product = [&](float (*out)[4], const float2 (*x)[2], int j, const float2 *f, float scale) {
+            // left rows times those of 16 tokens j
+            auto product = [&](float (*out)[4], const float2 (*x)[2], int j) {
                 uint32_t ah[4], al[4], bh_[2][2], bl[2][2];
+                const uint32_t at = right + 16 * j * (kRowLd * 4) + 32 * ks;
+                ldsm4(bh_[0], bh_[1], at);
+                ldsm4(bl[0], bl[1], at + 2 * kDK);
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const int col = 16 * ks + 8 * e + 2 * c;
                     dev::split_half(x[0][e], &ah[2 * e], &al[2 * e]);
                     dev::split_half(x[1][e], &ah[2 * e + 1], &al[2 * e + 1]);
-                    dev::split_half(times(pair(r.a[16 * j + g], col, r.ks[16 * j + g] * scale), f[e]), &bh_[0][e], &bl[0][e]);
-                    dev::split_half(times(pair(r.a[16 * j + g + 8], col, r.ks[16 * j + g + 8] * scale), f[e]), &bh_[1][e], &bl[1][e]);
                 }
 #pragma unroll
                 for (int e = 0; e < 2; e++) mma16816(out[e], al[0], al[1], al[2], al[3], bh_[e][0], bh_[e][1]);
@@ -792,26 +809,26 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
                 for (int e = 0; e < 2; e++) mma16816(out[e], ah[0], ah[1], ah[2], ah[3], bh_[e][0], bh_[e][1]);
             };
             if (fast) {
-                float2 x[2][2], f[2];
+                float2 x[2][2];
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const int col = 16 * ks + 8 * e + 2 * c;
-                    const float2 mid = *reinterpret_cast<const float2 *>(&r.mid[m][col]), all = *reinterpret_cast<const float2 *>(&r.blk[m][col]);
-                    const float2 inv = make_float2(kRoom / mid.x, kRoom / mid.y);
-                    x[0][e] = times(left[0][e], inv);
-                    x[1][e] = times(left[1][e], inv);
-                    f[e] = make_float2(mid.x / all.x, mid.y / all.y);
+                    const float2 inv = pair(r.inv[m], col + 8 * e);
+                    x[0][e] = __fmul2_rn(left[0][e], inv);
+                    x[1][e] = __fmul2_rn(left[1][e], inv);
                 }
-                product(own, x, m, f, kRoom);
+                product(own, x, m);
             }
-            float2 between[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
 #pragma unroll
             for (int j = 2; j >= 0; j--) {
                 if (j >= m) continue;
                 if (j + 1 < m)  // another 16 tokens between
 #pragma unroll
-                    for (int e = 0; e < 2; e++) between[e] = times(between[e], *reinterpret_cast<const float2 *>(&r.blk[j + 1][16 * ks + 8 * e + 2 * c]));
-                product(&acc[2 * j], left, j, between, 1.f);
+                    for (int e = 0; e < 2; e++) {
+                        const float2 f = pair(r.blk[j + 1], col + 8 * e);
+                        left[0][e] = __fmul2_rn(left[0][e], f);
+                        left[1][e] = __fmul2_rn(left[1][e], f);
+                    }
+                product(&acc[2 * j], left, j);
             }
         }
         // unscales: exact quotients of powers of two
@@ -826,7 +843,7 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
                 acc[j][0] *= f0 * kb.x; acc[j][1] *= f0 * kb.y; acc[j][2] *= f1 * kb.x; acc[j][3] *= f1 * kb.y;
             } else if (j < 2 * m + 2 && fast) {
                 const float *x = own[j & 1];
-                const float big = 1.f / (kRoom * kRoom);
+                const float big = 1.f / kRoom;
                 acc[j][0] = i + d <= g ? x[0] * (f0 * kb.x) * big : 0.f;
                 acc[j][1] = i + 1 + d <= g ? x[1] * (f0 * kb.y) * big : 0.f;
                 acc[j][2] = i + d <= g + 8 ? x[2] * (f1 * kb.x) * big : 0.f;

@@ -313,6 +313,29 @@ def test_prompt_long(G, variant, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["half", "near-half", "one-drop", "first", "last"])
+def test_prompt_gates_at_the_border(G, dtype, kind):
+    """16 tokens whose gates' product lies at 2^-16, evenly or in one step, with rows of k at the largest mantissa."""
+    def change(q, k, v, alpha, beta, St):
+        t = torch.arange(len(alpha), device="cuda").reshape(-1, 1, 1) % 16
+        one = torch.ones_like(alpha)
+        if kind == "half":
+            alpha = 0.5 * one
+        elif kind == "near-half":
+            alpha = 0.5 + 0.02 * (alpha - 0.75)
+        elif kind == "one-drop":
+            at = torch.arange(alpha.shape[2], device="cuda") % 16
+            alpha = torch.where(t == at, 2.0 ** -16, one)
+        else:
+            alpha = torch.where(t == (1 if kind == "first" else 15), 2.0 ** -16, one)
+        k = torch.where(k.float() < 0, -0.1249, 0.1249).to(k.dtype)  # just below 2^-3: rows of norm sqrt 2
+        return q, k, v, alpha, 0.5 * beta, St
+
+    run_prompt(G, KDA, DT[dtype], [70, 64, 17], 2, 1, [7, 0, 7], seed=19, change=change)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("variant", [GDN, KDA, LINEAR])
 @pytest.mark.parametrize("max_length", [8, None])
 @pytest.mark.parametrize("kind", ["open", "quick", "quicker", "shut", "tiny", "mixed", "nobeta", "onebeta", "zero", "small", "large"])
