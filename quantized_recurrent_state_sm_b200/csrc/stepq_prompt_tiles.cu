@@ -608,20 +608,19 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
         }
         const T *kg = static_cast<const T *>(a.k) + (long long)k.t0 * a.stride_k + hq * kDK + 4 * l, *qg = static_cast<const T *>(a.q) + (long long)k.t0 * a.stride_q + hq * kDK + 4 * l;
         float4 x[8], y[8];
+        // without branches, so that all loads are under way at once
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            const int row = 8 * w + i;
-            x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (row < k.n) {
-                x[i] = load4(kg + row * a.stride_k);
-                y[i] = load4(qg + row * a.stride_q);
-            }
+            const int row = min(8 * w + i, k.n - 1);
+            x[i] = load4(kg + row * a.stride_k);
+            y[i] = load4(qg + row * a.stride_q);
         }
         if (tid < 4) r.fast[tid] = 1;
         if (tid < kC) r.beta[tid] = tid < k.n ? a.beta[(long long)(k.t0 + tid) * a.heads + h] : 0.f;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const int row = 8 * w + i;
+            if (row >= k.n) x[i] = y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<float4 *>(&r.k[row][4 * l]) = x[i];
             *reinterpret_cast<float4 *>(&r.q[row][4 * l]) = y[i];
             float sk, sq, back;
@@ -781,25 +780,27 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
         const uint32_t right = dev::smem_addr(r.a[(l & 7) + (l >> 4) * 8]) + ((l >> 3) & 1) * 16;
         auto pair = [&](const float *row, int col) { return *reinterpret_cast<const float2 *>(row + col); };
         float own[2][4] = {};
-#pragma unroll 2
-        for (int ks = 0; ks < kDK / 16; ks++) {
-            const int col = 16 * ks + 2 * c;
-            float2 left[2][2];  // of rows g, g + 8: columns 2 c.., 2 c + 8..
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                left[0][e] = __fmul2_rn(pair(src[r0], col + 8 * e), make_float2(s0, s0));
-                left[1][e] = __fmul2_rn(pair(src[r1], col + 8 * e), make_float2(s1, s1));
-            }
-            // left rows times those of 16 tokens j
-            auto product = [&](float (*out)[4], const float2 (*x)[2], int j) {
+        // left rows (times rows of factors f) by those of 16 tokens j: a loop of its own for each j,
+        // so that the loads and halves of several steps overlap
+        auto product = [&](float (*out)[4], int j, const float (*f)[kDK], auto factors) {
+            const uint32_t at = right + 16 * j * (kRowLd * 4);
+#pragma unroll 4
+            for (int ks = 0; ks < kDK / 16; ks++) {
                 uint32_t ah[4], al[4], bh_[2][2], bl[2][2];
-                const uint32_t at = right + 16 * j * (kRowLd * 4) + 32 * ks;
-                ldsm4(bh_[0], bh_[1], at);
-                ldsm4(bl[0], bl[1], at + 2 * kDK);
+                ldsm4(bh_[0], bh_[1], at + 32 * ks);
+                ldsm4(bl[0], bl[1], at + 32 * ks + 2 * kDK);
 #pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    dev::split_half(x[0][e], &ah[2 * e], &al[2 * e]);
-                    dev::split_half(x[1][e], &ah[2 * e + 1], &al[2 * e + 1]);
+                for (int e = 0; e < 2; e++) {  // columns 2 c.., 2 c + 8..
+                    const int col = 16 * ks + 8 * e + 2 * c;
+                    float2 x0 = __fmul2_rn(pair(src[r0], col), make_float2(s0, s0)), x1 = __fmul2_rn(pair(src[r1], col), make_float2(s1, s1));
+#pragma unroll
+                    for (int i = 0; i < decltype(factors)::value; i++) {
+                        const float2 u = pair(f[i], col);
+                        x0 = __fmul2_rn(x0, u);
+                        x1 = __fmul2_rn(x1, u);
+                    }
+                    dev::split_half(x0, &ah[2 * e], &al[2 * e]);
+                    dev::split_half(x1, &ah[2 * e + 1], &al[2 * e + 1]);
                 }
 #pragma unroll
                 for (int e = 0; e < 2; e++) mma16816(out[e], al[0], al[1], al[2], al[3], bh_[e][0], bh_[e][1]);
@@ -807,29 +808,17 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
                 for (int e = 0; e < 2; e++) mma16816(out[e], ah[0], ah[1], ah[2], ah[3], bl[e][0], bl[e][1]);
 #pragma unroll
                 for (int e = 0; e < 2; e++) mma16816(out[e], ah[0], ah[1], ah[2], ah[3], bh_[e][0], bh_[e][1]);
-            };
-            if (fast) {
-                float2 x[2][2];
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    const float2 inv = pair(r.inv[m], col + 8 * e);
-                    x[0][e] = __fmul2_rn(left[0][e], inv);
-                    x[1][e] = __fmul2_rn(left[1][e], inv);
-                }
-                product(own, x, m);
             }
+        };
+        if (fast) product(own, m, &r.inv[m], std::integral_constant<int, 1>{});
 #pragma unroll
-            for (int j = 2; j >= 0; j--) {
-                if (j >= m) continue;
-                if (j + 1 < m)  // another 16 tokens between
-#pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const float2 f = pair(r.blk[j + 1], col + 8 * e);
-                        left[0][e] = __fmul2_rn(left[0][e], f);
-                        left[1][e] = __fmul2_rn(left[1][e], f);
-                    }
-                product(&acc[2 * j], left, j);
-            }
+        for (int j = 0; j < 3; j++) {  // the 16s between
+            if (j + 1 == m)
+                product(&acc[2 * j], j, nullptr, std::integral_constant<int, 0>{});
+            else if (j + 2 == m)
+                product(&acc[2 * j], j, &r.blk[j + 1], std::integral_constant<int, 1>{});
+            else if (j + 3 == m)
+                product(&acc[2 * j], j, &r.blk[j + 1], std::integral_constant<int, 2>{});
         }
         // unscales: exact quotients of powers of two
         const float f0 = (is_q ? 1.f : r.beta[r0]) / s0, f1 = (is_q ? 1.f : r.beta[r1]) / s1;
