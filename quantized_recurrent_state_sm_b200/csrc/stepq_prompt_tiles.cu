@@ -109,12 +109,16 @@ __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, con
 // ---- the inverse and the squares ---------------------------------------------
 //
 // A (strictly lower triangular, [64][64]) and P are held as accumulators: warp m
-// of 0-3 has rows 16 m .. of A, all columns, and warp m or m + 4 those of P.  With T = (I +
-// A)^-1 in blocks of 16: T_mm by substitution, then row by row
+// of 0-3 has rows 16 m .. of A, all columns, and warp m or 7 - m those of P.  With
+// T = (I + A)^-1 in blocks of 16: T_mm by substitution, then row by row
 //   T_m = T_mm - (T_mm A_m) T_(<m),
 // products on the tensor cores; P T likewise.  A left operand comes from the
 // accumulators of its own warp, a right one from halves in shared memory, whose
 // row scales (inner indices of the product) are multiplied into the left one.
+
+// Rows 16 m .. that a warp has: a warp of the second four shares its scheduler with
+// one of the first, and m + 1 blocks of columns count, so the orders are opposite.
+__device__ __forceinline__ int rows_of(int w) { return w < 4 ? w : 7 - w; }
 
 constexpr int kDiagLd = 20;
 struct Squares {
@@ -162,40 +166,45 @@ __device__ __forceinline__ void put_tiles(const float (*x)[4], int tiles, const 
             }
 }
 
-// out += x y: x an accumulator of `blocks` blocks of 16 columns (scaled), y the
-// rows of a lower-triangular square's blocks, out their column tiles.
-template <int N>
-__device__ __forceinline__ void times_square(float (*out)[4], const float (*x)[4], int blocks, const float *scale, const char *square, int first_row, bool lower)
+// One block of a product with T, in place: the 16 columns J of x (tiles 2 J and 2 J
+// + 1) times T's 16 rows J, which reach columns 16 J + 15.  The columns before hold
+// what earlier blocks gave and are added to; those of J itself are done with and
+// hold their sum's first share.
+template <int J>
+__device__ __forceinline__ void add_block(float (*x)[4], const Squares &sq)
 {
-    const int l = threadIdx.x & 31;
-    const uint32_t y0 = dev::smem_addr(square);
+    const int l = threadIdx.x & 31, c = l & 3;
+    float y[2][4], scale[2], back[2];
 #pragma unroll
-    for (int i = 0; i < N / 2; i++) {
-        if (i >= blocks) continue;
-        uint32_t hi[4], lo[4];
+    for (int e = 0; e < 2; e++) {
+        const float2 f = *reinterpret_cast<const float2 *>(&sq.t_back[16 * J + 8 * e + 2 * c]);
+        y[e][0] = x[2 * J + e][0] * f.x; y[e][1] = x[2 * J + e][1] * f.y; y[e][2] = x[2 * J + e][2] * f.x; y[e][3] = x[2 * J + e][3] * f.y;
+    }
+    row_scales<2>(y, 2, scale, back);
+    uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-            dev::split_half(x[2 * i + e][0] * scale[0], x[2 * i + e][1] * scale[0], &hi[2 * e], &lo[2 * e]);
-            dev::split_half(x[2 * i + e][2] * scale[1], x[2 * i + e][3] * scale[1], &hi[2 * e + 1], &lo[2 * e + 1]);
-        }
-        const int tiles = lower ? 2 * i + 2 : N;
-        uint32_t b[N][2], d[N][2];
+    for (int e = 0; e < 2; e++) {
+        dev::split_half(y[e][0] * scale[0], y[e][1] * scale[0], &hi[2 * e], &lo[2 * e]);
+        dev::split_half(y[e][2] * scale[1], y[e][3] * scale[1], &hi[2 * e + 1], &lo[2 * e + 1]);
+    }
+    const uint32_t y0 = dev::smem_addr(sq.t);
 #pragma unroll
-        for (int j = 0; j < N; j += 2)
-            if (j < tiles) {
-                const uint32_t at = y0 + square_at(first_row + 16 * i + (l & 15), 8 * j + (l >> 4) * 8);
-                ldsm4_t(b[j], b[j + 1], at);
-                ldsm4_t(d[j], d[j + 1], at + kSquareBytes / 2);
-            }
+    for (int j = 0; j < 2 * J + 2; j += 2) {
+        uint32_t b[2][2], d[2][2];
+        float p[2][4] = {};
+        const uint32_t at = y0 + square_at(16 * J + (l & 15), 8 * j + (l >> 4) * 8);
+        ldsm4_t(b[0], b[1], at);
+        ldsm4_t(d[0], d[1], at + kSquareBytes / 2);
 #pragma unroll
-        for (int j = 0; j < N; j++)
-            if (j < tiles) mma16816(out[j], lo[0], lo[1], lo[2], lo[3], b[j][0], b[j][1]);
+        for (int e = 0; e < 2; e++) mma16816(p[e], lo[0], lo[1], lo[2], lo[3], b[e][0], b[e][1]);
 #pragma unroll
-        for (int j = 0; j < N; j++)
-            if (j < tiles) mma16816(out[j], hi[0], hi[1], hi[2], hi[3], d[j][0], d[j][1]);
+        for (int e = 0; e < 2; e++) mma16816(p[e], hi[0], hi[1], hi[2], hi[3], d[e][0], d[e][1]);
 #pragma unroll
-        for (int j = 0; j < N; j++)
-            if (j < tiles) mma16816(out[j], hi[0], hi[1], hi[2], hi[3], b[j][0], b[j][1]);
+        for (int e = 0; e < 2; e++) mma16816(p[e], hi[0], hi[1], hi[2], hi[3], b[e][0], b[e][1]);
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) x[j + e][i] = j == 2 * J ? p[e][i] * back[i >> 1] : fmaf(p[e][i], back[i >> 1], x[j + e][i]);
     }
 }
 
@@ -204,7 +213,7 @@ __device__ __forceinline__ void times_square(float (*out)[4], const float (*x)[4
 template <bool DELTA, int PW>
 __device__ __forceinline__ void finish(float (*acc)[4], float (*accp)[4], Squares &sq)
 {
-    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3, m = w & 3;
+    const int tid = threadIdx.x, w = tid >> 5, l = tid & 31, g = l >> 2, c = l & 3, m = rows_of(w);
     float scale[2], back[2];
     if constexpr (DELTA) {
         if (w < 4) {
@@ -295,55 +304,45 @@ __device__ __forceinline__ void finish(float (*acc)[4], float (*accp)[4], Square
                 }
             }
         }
-        __syncthreads();
-#pragma unroll 1
-        for (int mm = 1; mm < 4; mm++) {
-            if (w == mm) {
+        // T_0 is there.  Where T_j is, every later row takes its share of it at once,
+        // and the next row is complete; P T grows beside, the warp that makes the next
+        // row one turn behind.
+        const bool has_p = w >= PW;
+        auto turn = [&](auto J) {
+            constexpr int j = decltype(J)::value;
+            __syncthreads();
+            if constexpr (j < 3) {
+                if (w < 4 && m > j) add_block<j>(acc, sq);
+                if (w < 4 && m == j + 1) {
 #pragma unroll
-                for (int j = 0; j < 6; j++) {
-                    if (j >= 2 * mm) continue;
-                    const float2 f = *reinterpret_cast<const float2 *>(&sq.t_back[8 * j + 2 * c]);
-                    acc[j][0] *= f.x; acc[j][1] *= f.y; acc[j][2] *= f.x; acc[j][3] *= f.y;
-                }
-                row_scales<6>(acc, 2 * mm, scale, back);
-                float t[8][4] = {};
-                times_square<6>(t, acc, mm, scale, sq.t, 0, true);
+                    for (int i = 0; i < 2 * j + 2; i++)
 #pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    t[j][0] *= -back[0]; t[j][1] *= -back[0]; t[j][2] *= -back[1]; t[j][3] *= -back[1];
-                    if ((j & ~1) == 2 * mm)
+                        for (int e = 0; e < 4; e++) acc[i][e] = -acc[i][e];
 #pragma unroll
-                        for (int e = 0; e < 4; e++) t[j][e] = td[j & 1][e];
-                }
-                row_scales<8>(t, 2 * mm + 2, scale, back);
-                put_tiles<8>(t, 2 * mm + 2, scale, sq.t, mm);
-                if (c == 0) {
-                    sq.t_back[16 * mm + g] = back[0];
-                    sq.t_back[16 * mm + g + 8] = back[1];
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) acc[2 * j + 2 + e][i] = td[e][i];
+                    row_scales<2 * j + 4>(acc, 2 * j + 4, scale, back);
+                    put_tiles<2 * j + 4>(acc, 2 * j + 4, scale, sq.t, j + 1);
+                    if (c == 0) {
+                        sq.t_back[16 * (j + 1) + g] = back[0];
+                        sq.t_back[16 * (j + 1) + g + 8] = back[1];
+                    }
                 }
             }
-            __syncthreads();
-        }
+            if constexpr (PW == 0 && j > 0) {
+                if (m == j) add_block<j - 1>(accp, sq);
+            }
+            if (has_p && m >= j && !(PW == 0 && m == j + 1)) add_block<j>(accp, sq);
+        };
+        turn(std::integral_constant<int, 0>{});
+        turn(std::integral_constant<int, 1>{});
+        turn(std::integral_constant<int, 2>{});
+        turn(std::integral_constant<int, 3>{});
     }
     if (w >= PW && w < PW + 4) {
-        float o[8][4] = {};
-        if constexpr (DELTA) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                if (j >= 2 * m + 2) continue;
-                const float2 f = *reinterpret_cast<const float2 *>(&sq.t_back[8 * j + 2 * c]);
-                accp[j][0] *= f.x; accp[j][1] *= f.y; accp[j][2] *= f.x; accp[j][3] *= f.y;
-            }
-            row_scales<8>(accp, 2 * m + 2, scale, back);
-            times_square<8>(o, accp, m + 1, scale, sq.t, 0, true);
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                o[j][0] *= back[0]; o[j][1] *= back[0]; o[j][2] *= back[1]; o[j][3] *= back[1];
-            }
-        }
-        const float(*out)[4] = DELTA ? o : accp;
-        row_scales<8>(out, 2 * m + 2, scale, back);
-        put_tiles<8>(out, 2 * m + 2, scale, sq.a, m);
+        row_scales<8>(accp, 2 * m + 2, scale, back);
+        put_tiles<8>(accp, 2 * m + 2, scale, sq.a, m);
         if (c == 0) {
             sq.p_back[16 * m + g] = back[0];
             sq.p_back[16 * m + g + 8] = back[1];
@@ -563,9 +562,10 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
 // what is left at the end of its 16, whose halves are made once.  Gates, K and Q
 // are held in fp32, and give their places to the multiplied rows: what is needed
 // of shared memory decides how many CTAs lie side by side (two).
-// Measured: bf16, 105 blocks of 32 heads 298 us, 540 MB moved.  With the right
-// operand's halves made by each warp that reads it 343 us, and with every 16
-// tokens multiplied out 371 us.
+// Measured: bf16, 105 blocks of 32 heads 261 us, 540 MB moved; a CTA takes 44
+// thousand cycles, of which loads 10, products 10, the inverse and squares 13.
+// With the right operand's halves made by each warp that reads it the kernel took
+// 343 us, and with every 16 tokens multiplied out 371 us.
 // ---------------------------------------------------------------------------
 constexpr int kGateThreads = 256;
 constexpr int kRowLd = kDK + 4;  // row of a [64][128] fp32 matrix
@@ -769,8 +769,8 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
     }
     __syncthreads();
     // rows of 16 tokens m against those of the earlier 16s and their own, K by
-    // warps 0-3, Q by 4-7
-    const int m = w & 3;
+    // warps 0-3, Q by 4-7 in the opposite order
+    const int m = rows_of(w);
     const bool is_q = w >= 4, fast = r.fast[m] != 0;
     float acc[kC / 8][4] = {};
     {
