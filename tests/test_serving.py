@@ -599,6 +599,45 @@ def test_beam_select_strided_and_unaligned_rows(G):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("variant", [GDN, KDA, LINEAR])
+def test_calls_behind_one_another(G, variant):
+    """Prompts and selections without a wait between them, which get the same scratch in turn: each as if alone."""
+    sets = []
+    for seed, lengths in enumerate([[130, 5, 64], [1, 200, 70]]):
+        q, k, v, alpha, beta, St = prompt_inputs(variant, torch.bfloat16, lengths, 4, 2, seed)
+        p = G.RequestPlan(3, sum(lengths))
+        p.build(i32(lengths), i32([7, 0, 7]))
+        x = torch.randn((3, 4, 9001), device="cuda")
+        sets.append((p, q, k, v, alpha, beta, St, x, -torch.rand((3, 4), device="cuda")))
+
+    def both(p, q, k, v, alpha, beta, St, x, s):
+        St = St.clone()
+        return [G.prompt(variant, p, q, k, v, alpha, beta, St), St, *G.beam_select(x, s)]
+
+    alone = []
+    for x in sets:
+        alone.append(both(*x))
+        torch.cuda.synchronize()
+    got = [both(*sets[i % 2]) for i in range(24)]
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(outs, alone[i % 2]))
+    # and captured: a graph of the same calls, replayed twice without a wait
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        both(*sets[0])
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = [both(*sets[i % 2]) for i in range(4)]
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, outs in enumerate(kept):
+        assert all(torch.equal(a, b) for a, b in zip(outs, alone[i % 2]))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("groups,beams,row", [(1, 1, 16), (3, 2, 48), (2, 5, 1040), (4, 8, 33 * 1024), (1, 64, 4112), (7, 3, 5 * 16)])
 def test_reorder_rows(G, groups, beams, row):
     rng = np.random.default_rng(beams)
