@@ -71,6 +71,9 @@ __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.
 // acc[j] = rows 16 m .. 16 m + 15 of A times rows 8 j .. of B transposed, for
 // the column tiles j < tiles (a multiple of 2): A and B operand tiles in
 // shared memory.  Each pass goes over all sums before it returns to the first.
+// Where products are three, the loop's turns stay apart, for its instructions to
+// stay near (prompts of 16 requests in fp32 265 us instead of 271); of one, not
+// (one long prompt in bf16 592 us instead of 598).
 template <int NP>
 __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, const char *B, int m, int tiles)
 {
@@ -78,7 +81,7 @@ __device__ __forceinline__ void rows_product(float (*acc)[4], const char *A, con
     const uint32_t a0 = dev::smem_addr(A), b0 = dev::smem_addr(B);
     const int arow = 16 * m + (l & 7) + ((l >> 3) & 1) * 8, acol = (l >> 4) * 8;  // of the A matrices
     const int brow = (l & 7) + (l >> 4) * 8, bcol = ((l >> 3) & 1) * 8;           // of two column tiles
-#pragma unroll
+#pragma unroll(NP == 2 ? 1 : kDK / 16)
     for (int i = 0; i < kDK / 16; i++) {
         uint32_t ah[4], al[4];
         ldsm4(ah, a0 + tile_at(arow, 16 * i + acol));
@@ -386,7 +389,7 @@ __device__ __forceinline__ bool find_block(const PromptArgs &a, int first_block,
 // tokens, of the 16s between, and of t's 16 up to t; inside 16 tokens it is
 // multiplied out.
 // Measured: bf16, 128 blocks of 32 heads 121 us, 214 MB moved (47 % issue, 14 %
-// of the tensor pipe); fp32, 101 blocks of 32 heads 155 us, where all products
+// of the tensor pipe); fp32, 101 blocks of 32 heads 150 us, where all products
 // are three; plain, binary16, 64 blocks of 32 heads 31 us, without the inverse.
 // ---------------------------------------------------------------------------
 constexpr int kTileThreads = 128;
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(kTileThreads, NP == 1 ? 4 : 3) k_block_tiles(P
 // what is left at the end of its 16, whose halves are made once.  Gates, K and Q
 // are held in fp32, and give their places to the multiplied rows: what is needed
 // of shared memory decides how many CTAs lie side by side (two).
-// Measured: bf16, 105 blocks of 32 heads 261 us, 540 MB moved; a CTA takes 44
+// Measured: bf16, 105 blocks of 32 heads 256 us, 540 MB moved; a CTA takes 44
 // thousand cycles, of which loads 10, products 10, the inverse and squares 13.
 // With the right operand's halves made by each warp that reads it the kernel took
 // 343 us, and with every 16 tokens multiplied out 371 us.
@@ -781,10 +784,11 @@ __global__ void __launch_bounds__(kGateThreads, 2) k_gate_tiles(PromptArgs a, in
         auto pair = [&](const float *row, int col) { return *reinterpret_cast<const float2 *>(row + col); };
         float own[2][4] = {};
         // left rows (times rows of factors f) by those of 16 tokens j: a loop of its own for each j,
-        // so that the loads and halves of several steps overlap
+        // so that the loads and halves of two steps overlap (eight take 391 us instead
+        // of 376 for prompts of 16 requests: more instructions than lie near)
         auto product = [&](float (*out)[4], int j, const float (*f)[kDK], auto factors) {
             const uint32_t at = right + 16 * j * (kRowLd * 4);
-#pragma unroll 4
+#pragma unroll 2
             for (int ks = 0; ks < kDK / 16; ks++) {
                 uint32_t ah[4], al[4], bh_[2][2], bl[2][2];
                 ldsm4(bh_[0], bh_[1], at + 32 * ks);
